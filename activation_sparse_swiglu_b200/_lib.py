@@ -17,6 +17,9 @@ STATUS_NAMES = {0: "PROX_OK", 1: "PROX_EINVAL", 2: "PROX_ENOMEM", 3: "PROX_ECUDA
                 4: "PROX_EUNSUPPORTED", 5: "PROX_EDEVICE"}
 DEVERR_MASK_INDEX = 0x1
 DEVERR_WAIT_TIMEOUT = 0x2
+DEVERR_SLOT = 0x4
+DEVERR_PAGE = 0x8
+DEVERR_LEN = 0x10
 
 
 class ProxError(RuntimeError):
@@ -42,6 +45,7 @@ MASK_TOPK = 0
 MASK_THRESHOLD = 1
 ACT_SILU, ACT_GELU_TANH, ACT_GELU_ERF = 0, 1, 2
 STAGE2_EXACT, STAGE2_PROXY_VALUES = 0, 1
+DTYPE_F32, DTYPE_F16, DTYPE_BF16 = 0, 1, 2
 
 
 _P = ctypes.c_void_p
@@ -79,6 +83,17 @@ SIGNATURES = {
     "prox_debug_batch_masks": (_I, [_P, _P, _I, _P]),
     "prox_ffn_forward_host": (_I, [_P, _P, _P, _I, _P]),
     "prox_ffn_forward_profiled": (_I, [_P, _P, _P, ctypes.POINTER(_P), _P, _P]),
+    "prox_linear4_create": (_I, [_P, _P, _I, _I, _P, ctypes.POINTER(_P)]),
+    "prox_linear4_create_bf16": (_I, [_P, _I, _I, _P, ctypes.POINTER(_P)]),
+    "prox_linear4_destroy": (_I, [_P]),
+    "prox_linear4_forward": (_I, [_P, _P, _L, _P, _L, _I, _I, _P]),
+    "prox_kv4_create": (_I, [_P, _P, _P, _P, _I, _I, _I, _I, ctypes.POINTER(_P)]),
+    "prox_kv4_destroy": (_I, [_P]),
+    "prox_kv4_error": (_I, [_P, ctypes.POINTER(ctypes.c_int32), _P]),
+    "prox_kv4_append": (_I, [_P, _P, _P, _L, _L, _L, _L, _P, _I, _I, _P]),
+    "prox_kv4_read": (_I, [_P, _P, _I, _P, _P, _I, _P]),
+    "prox_kv4_attend": (_I, [_P, _P, _L, _L, _L, _I, _I, _I, _P, _L, _I, _P, _F, _P, _P, _I, _P]),
+    "prox_plan_pages": (_I, [_P, _P, _I, _I, _P, _L, _I, _P, _I, _P, _P, _P, _P, _P, _P, _I, _P, _P]),
     "prox_debug_stage1": (_I, [_P, _P, _P, _P, _P, _P, _P, _P]),
     "prox_layer_proxy_scores": (_I, [_P, _P, _I, _P, _P]),
     "prox_debug_mask": (_I, [_P, _P, _P, _P, _P]),

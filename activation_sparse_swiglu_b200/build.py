@@ -18,9 +18,10 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(PKG, "libprox.so")
 
-SOURCES = ["prox_api.cu", "token.cu", "batch.cu", "pack.cu", "calibrate.cu", "misc.cu"]
+SOURCES = ["prox_api.cu", "token.cu", "batch.cu", "pack.cu", "calibrate.cu", "misc.cu",
+           "decode4_api.cu", "linear4.cu", "kv4.cu", "attend4.cu", "pages.cu"]
 HEADERS = ["prox_device.cuh", "prox_internal.h", "select.cuh", "token_args.cuh", "stage1.cuh",
-           "stage2.cuh"]
+           "stage2.cuh", "api_util.h", "decode4.h", "quant4.cuh"]
 
 NVCC_FLAGS = [
     "-gencode", "arch=compute_100a,code=sm_100a",

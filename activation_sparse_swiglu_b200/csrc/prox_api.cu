@@ -10,8 +10,11 @@
 #include <new>
 #include <string>
 
+#include "api_util.h"
 #include "prox_device.cuh"
 #include "prox_internal.h"
+
+using namespace prox::api;
 
 namespace {
 
@@ -57,6 +60,11 @@ thread_local std::string g_last_error;
 // count to zero fails as if the device were out of memory.
 std::atomic<int> g_alloc_countdown{0};
 
+}  // namespace
+
+namespace prox {
+namespace api {
+
 cudaError_t dev_alloc(void** p, size_t bytes) {
   int c = g_alloc_countdown.load();
   while (c > 0 && !g_alloc_countdown.compare_exchange_weak(c, c - 1)) {
@@ -66,13 +74,6 @@ cudaError_t dev_alloc(void** p, size_t bytes) {
     return cudaErrorMemoryAllocation;
   }
   return cudaMalloc(p, bytes);
-}
-template <typename T>
-cudaError_t dev_alloc(T** p, size_t bytes) {
-  void* v = nullptr;
-  const cudaError_t e = dev_alloc(&v, bytes);
-  *p = static_cast<T*>(v);
-  return e;
 }
 
 prox_status fail(prox_status st, const char* fmt, ...) {
@@ -91,27 +92,6 @@ prox_status cuda_fail(cudaError_t e, const char* what) {
               cudaGetErrorString(e));
 }
 
-#define PROX_CUDA(call, what)                         \
-  do {                                                \
-    cudaError_t e_ = (call);                          \
-    if (e_ != cudaSuccess) return cuda_fail(e_, what); \
-  } while (0)
-
-bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
-bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
-
-cudaStream_t as_stream(void* s) { return reinterpret_cast<cudaStream_t>(s); }
-
-prox_status check_shape(int d, int F) {
-  if (d <= 0 || d % prox::kGroup != 0 || d > prox::kMaxDModel)
-    return fail(PROX_EINVAL, "d_model=%d must be a positive multiple of 128 and <= %d", d,
-                prox::kMaxDModel);
-  if (F <= 0 || F % 32 != 0 || F > prox::kMaxDff)
-    return fail(PROX_EINVAL, "d_ff=%d must be a positive multiple of 32 and <= %d", F,
-                prox::kMaxDff);
-  return PROX_OK;
-}
-
 prox_status check_device(int* dev, int* sms) {
   PROX_CUDA(cudaGetDevice(dev), "cudaGetDevice");
   int major = 0;
@@ -123,7 +103,20 @@ prox_status check_device(int* dev, int* sms) {
   return PROX_OK;
 }
 
-size_t align256(size_t x) { return (x + 255) & ~(size_t)255; }
+}  // namespace api
+}  // namespace prox
+
+namespace {
+
+prox_status check_shape(int d, int F) {
+  if (d <= 0 || d % prox::kGroup != 0 || d > prox::kMaxDModel)
+    return fail(PROX_EINVAL, "d_model=%d must be a positive multiple of 128 and <= %d", d,
+                prox::kMaxDModel);
+  if (F <= 0 || F % 32 != 0 || F > prox::kMaxDff)
+    return fail(PROX_EINVAL, "d_ff=%d must be a positive multiple of 32 and <= %d", F,
+                prox::kMaxDff);
+  return PROX_OK;
+}
 
 void free_layer_buffers(prox_layer* L) {
   if (L->wgu) cudaFree(L->wgu);

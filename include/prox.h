@@ -65,6 +65,10 @@ typedef enum prox_status {
 /* Device error word bits (prox_layer_error). */
 #define PROX_DEVERR_MASK_INDEX 0x1  /* a channel index outside [0, d_ff) */
 #define PROX_DEVERR_WAIT_TIMEOUT 0x2 /* a bounded pipeline wait ran out */
+/* Error word bits of a 4-bit cache (prox_kv4_error). */
+#define PROX_DEVERR_SLOT 0x4 /* a slot past the cache's last one */
+#define PROX_DEVERR_PAGE 0x8 /* a table entry outside [0, num_pages) */
+#define PROX_DEVERR_LEN 0x10 /* a length below 0 or past the table's columns */
 
 typedef struct prox_layer prox_layer; /* opaque */
 
@@ -354,6 +358,143 @@ PROX_API prox_status prox_ffn_forward_host(prox_layer* layer, const float* x_hos
 PROX_API prox_status prox_ffn_forward_profiled(const prox_layer* layer, const float* x, float* out,
                                                void* const* events_host, uint64_t* phase_ns,
                                                void* stream);
+
+/* ------------------------------------------------------------------------
+ * 4-bit operators of the rest of the decoder block
+ *
+ * What a decode step runs beside its FFN, on operands held in the packer's
+ * INT4 format (Prox §4.3; offset-binary codes q + 8, fp16 scales): the
+ * projections (prox_linear4_*), a paged cache of keys and values with the
+ * attention that reads it (prox_kv4_*), and the plan that says which cache
+ * pages and slots a step's tokens take (prox_plan_pages).  The Prox pages have
+ * no counterpart: they leave attention and its projections as they are
+ * (App. A.5 times them beside the FFN).
+ *
+ * Activations may be fp32, fp16 or bf16 (PROX_F32 / F16 / BF16); results have
+ * the type of the inputs, are accumulated in fp32 and rounded once.
+ * ------------------------------------------------------------------------ */
+#define PROX_F32 0
+#define PROX_F16 1
+#define PROX_BF16 2
+
+typedef struct prox_linear4 prox_linear4; /* opaque: INT4 weights of one matrix */
+typedef struct prox_kv4 prox_kv4;         /* opaque: a 4-bit cache and its workspace */
+
+/* INT4 weights of one [d_in, d_out] matrix, repacked into library-owned memory
+ * in the order the product reads them.  codes, scales: as prox_pack_proxy
+ * writes them (uint8 [d_in, d_out/2], low nibble = even channel, code q + 8
+ * with q in [-8, 7]; fp16 [d_in/128, d_out]), 2-byte aligned scales.
+ * d_in a positive multiple of 128 and at most 65536, d_out positive, even and
+ * at most 2^20.  Inputs may be freed once the call returns (it synchronises
+ * `stream`). */
+PROX_API prox_status prox_linear4_create(const uint8_t* codes, const uint16_t* scales, int d_in, int d_out,
+                                         void* stream, prox_linear4** out_host);
+
+/* The same from a bf16 weight W [d_in, d_out], 4-byte aligned, quantised by
+ * the rule of prox_pack_proxy. */
+PROX_API prox_status prox_linear4_create_bf16(const uint16_t* W, int d_in, int d_out, void* stream,
+                                              prox_linear4** out_host);
+
+/* Frees the weights (as prox_layer_destroy) and the handle; NULL is accepted. */
+PROX_API prox_status prox_linear4_destroy(prox_linear4* lin);
+
+/* out[b, n] = sum_g scales[g, n] sum_{k in g} q[k, n] x[b, k] for B tokens,
+ * 1 <= B <= 16.  x: [B, d_in] and out: [B, d_out] of `dtype`, rows x_stride
+ * and out_stride elements apart (at least d_in / d_out; out may not overlap
+ * x).  fp16 and bf16 inputs enter the products exactly, fp32 inputs with 22
+ * significant bits; sums are fp32.  A token with an infinity or NaN has
+ * non-finite results; other tokens are not touched by it.  Results do not
+ * depend on timing; no scratch is shared, so calls on one handle may overlap.
+ * Allocates nothing and does not synchronise. */
+PROX_API prox_status prox_linear4_forward(const prox_linear4* lin, const void* x, int64_t x_stride, void* out,
+                                          int64_t out_stride, int B, int dtype, void* stream);
+
+/* A paged 4-bit cache over caller-owned tensors:
+ *   k_codes, v_codes: uint8 [num_pages, n_heads, page_size, head_dim/2], low
+ *     nibble = even element, code q + 8;
+ *   k_scales, v_scales: fp16 [num_pages, n_heads, page_size];
+ *   element d of a row is q[d] * scale.
+ * head_dim 64, 128 or 256; page_size 16, 32, 64, 128 or 256; codes 16-byte
+ * and scales 32-byte aligned.  Slot s is row s % page_size of page
+ * s / page_size.  The handle owns an error word and the attention's workspace,
+ * so one stream at a time may use it; the tensors must outlive it. */
+PROX_API prox_status prox_kv4_create(uint8_t* k_codes, uint16_t* k_scales, uint8_t* v_codes, uint16_t* v_scales,
+                                     int num_pages, int n_heads, int page_size, int head_dim, prox_kv4** out_host);
+
+/* Frees the workspace and the handle (not the cache tensors); NULL is accepted. */
+PROX_API prox_status prox_kv4_destroy(prox_kv4* cache);
+
+/* Reads and clears the cache's error word (PROX_DEVERR_SLOT / PAGE / LEN);
+ * synchronises `stream`. */
+PROX_API prox_status prox_kv4_error(prox_kv4* cache, int32_t* word_host, void* stream);
+
+/* Quantises T new rows of keys and values into the cache.  Row (t, h) of k
+ * starts k_token * t + k_head * h elements into it and holds head_dim
+ * contiguous values of `dtype`; v likewise.  slots: int64 [T]; a negative slot
+ * skips its token, a slot past the cache sets PROX_DEVERR_SLOT and skips it;
+ * two tokens of one call may not share a slot.  Per row: scale =
+ * fp16_nearest_even(fp32(amax / 7)), q = clamp(x / scale rounded half to even,
+ * -7, 7), 0 where the scale is 0.  A NaN in a row makes its scale NaN (the row
+ * reads back as NaN); so does an infinity or amax/7 past the fp16 range, as an
+ * infinite scale.  T >= 0. */
+PROX_API prox_status prox_kv4_append(const prox_kv4* cache, const void* k, const void* v, int64_t k_token,
+                                     int64_t k_head, int64_t v_token, int64_t v_head, const int64_t* slots, int T,
+                                     int dtype, void* stream);
+
+/* The values the cache holds at `slots` (int64 [T]) into k_out and v_out
+ * [T, n_heads, head_dim] of `dtype`, contiguous and 16-byte aligned; zeros for
+ * negative slots, and for slots past the cache (PROX_DEVERR_SLOT). */
+PROX_API prox_status prox_kv4_read(const prox_kv4* cache, const int64_t* slots, int T, void* k_out, void* v_out,
+                                   int dtype, void* stream);
+
+/* Attention of the newest Tq tokens of each of B requests over the cache:
+ *   out[b, i, h] = sum_j softmax_j(scale q[b, i, h] . K[j, h']) V[j, h'],
+ * h' = h / (n_q_heads / n_heads), over the rows j <= lens[b] - Tq + i of the
+ * request; its row j is row j % page_size of page table[b, j / page_size].
+ * lens (int32 [B]) counts the new tokens, which must be in the cache.  A query
+ * that sees no row (lens[b] - Tq + i < 0) gives zeros and lse = -inf.
+ * Nothing behind a request's last row is used, whatever it holds.
+ * q: [B, Tq, n_q_heads, head_dim] of `dtype` with the given strides (elements;
+ * the last dimension contiguous); out: contiguous, 16-byte aligned, the same
+ * type; lse (may be NULL): fp32 [B, Tq, n_q_heads], log sum_j exp(scale q.K_j).
+ * table: int32 [B, cols], rows table_stride apart; entries behind a request's
+ * last page are not read.  n_q_heads a multiple of n_heads; 1 <= B <= 8192;
+ * Tq >= 1; scale finite.  An entry outside [0, num_pages) sets
+ * PROX_DEVERR_PAGE, a length outside [0, cols * page_size] PROX_DEVERR_LEN;
+ * that request's result is then meaningless, and no memory outside the cache
+ * is touched.  Scores, softmax statistics and sums are fp32; fp16 and bf16
+ * queries enter the products exactly and probabilities with 11 bits, for fp32
+ * both carry 22.  Results do not depend on timing. */
+PROX_API prox_status prox_kv4_attend(const prox_kv4* cache, const void* q, int64_t q_req, int64_t q_tok,
+                                     int64_t q_head, int n_q_heads, int B, int Tq, const int32_t* table,
+                                     int64_t table_stride, int cols, const int32_t* lens, float scale, void* out,
+                                     float* lse, int dtype, void* stream);
+
+/* Plans the cache rows of one step on the GPU.  Request i holds lens[i] tokens
+ * in the pages table[i, 0 .. ceil(lens[i] / page_size)) and gains (delta[i] >
+ * 0) or drops its newest (delta[i] < 0; all of them when it is finished)
+ * tokens.  free_pages[0 .. *free_count) are the free pages.
+ *   1. pages that rows no longer need are appended to free_pages, rows in
+ *      order, each row's in order;
+ *   2. pages that rows gain are taken off its end, in the same order, and
+ *      entered in table;
+ *   3. lens_out[i] = lens[i] + delta[i]; *free_count_out; cu[i] (int32 [B + 1])
+ *      = the new tokens of the requests before i; for new token n of the step:
+ *      slots[n] (int64) and positions[n] (int32); -1 in both for n behind the
+ *      last one (n < max_new).
+ * *status = 1, lens and the count unchanged, cu = 0, slots and positions -1,
+ * and table and free_pages untouched, when the plan does not fit: a length
+ * below 0 or past cols * page_size before or after, too few free pages, more
+ * than max_new new tokens, or more returned pages than free_pages has room for
+ * (free_cap entries).  lens_out may be lens, and free_count_out free_count (a
+ * plan that is committed at once); otherwise the same plan may be made again.
+ * Freed table entries keep their values.  1 <= B <= 8192, page_size >= 1,
+ * cols >= 0, B * cols < 2^31; all int32 unless said; device pointers. */
+PROX_API prox_status prox_plan_pages(const int32_t* lens, const int32_t* delta, int B, int page_size, int32_t* table,
+                                     int64_t table_stride, int cols, int32_t* free_pages, int free_cap,
+                                     const int32_t* free_count, int32_t* lens_out, int32_t* free_count_out,
+                                     int32_t* cu, int64_t* slots, int32_t* positions, int max_new, int32_t* status,
+                                     void* stream);
 
 /* ------------------------------------------------------------------------
  * Test taps: the same kernels, exposing intermediate results
