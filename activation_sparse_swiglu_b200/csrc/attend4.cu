@@ -215,15 +215,15 @@ __global__ void __launch_bounds__(kMaxWarps * 32, 1) attend4_kernel(const Attend
       if (tok0 + row < s.len) {
         const int64_t r = ((int64_t)((row < 16 ? pid[0] : pid[1])) * a.heads + head << a.page_shift) +
                           ((tok0 + row) & page_mask);
-        cp_async16(dst + k_piece<D>(row, j), a.k + r * (D / 2) + 16 * j);
-        cp_async16(dst + kStep * D / 2 + v_piece<D>(row, j), a.v + r * (D / 2) + 16 * j);
+        cp_async16(smem_u32(dst) + k_piece<D>(row, j), a.k + r * (D / 2) + 16 * j);
+        cp_async16(smem_u32(dst) + kStep * D / 2 + v_piece<D>(row, j), a.v + r * (D / 2) + 16 * j);
       }
     }
     if (lane < 8) {  // scales: four pieces of 8 tokens each
       const int q = lane & 3;
       if (tok0 + 8 * q < s.len) {
         const int64_t r = ((int64_t)(pid[q >> 1]) * a.heads + head << a.page_shift) + ((tok0 + 8 * q) & page_mask);
-        cp_async16(dst + kStep * D + (lane >> 2) * kStep * 2 + 16 * q, (lane < 4 ? a.ks : a.vs) + r);
+        cp_async16(smem_u32(dst) + kStep * D + (lane >> 2) * kStep * 2 + 16 * q, (lane < 4 ? a.ks : a.vs) + r);
       }
     }
   };

@@ -18,10 +18,10 @@ constexpr int kAttendMaxRequests = 8192;  // bounds the attention's table of chu
 }  // namespace prox
 
 // INT4 weights [K, N] in the order the product's fragments need:
-// codes [S][G][2][32][16 B] (S = tiles of 16 channels, G = groups of 128 input
-// rows), scales fp16 [S][G][8][2].
+// by strips of 32 channels and groups of 128 input rows, 2 KB of codes and 64
+// bytes of scales each (linear4.cu has the order inside).
 struct prox_linear4 {
-  int K = 0, N = 0, G = 0, S = 0;
+  int K = 0, N = 0, G = 0, strips = 0;
   int device = 0, num_sms = 0;
   int clusters[4] = {0, 0, 0, 0};  // clusters of 1, 2, 4, 8 CTAs that are resident at once
   uint8_t* codes = nullptr;

@@ -59,10 +59,10 @@ prox_status linear4_new(int d_in, int d_out, prox_linear4** out) {
   L->K = d_in;
   L->N = d_out;
   L->G = d_in / prox::kGroupRows;
-  L->S = (d_out + 31) / 32 * 2;  // tiles of 16 channels, in pairs
+  L->strips = (d_out + 31) / 32;
   L->device = dev;
   L->num_sms = sms;
-  const size_t units = (size_t)L->S * L->G, code_bytes = units * 1024, scale_bytes = units * 32;
+  const size_t units = (size_t)L->strips * L->G, code_bytes = units * 2048, scale_bytes = units * 64;
   cudaError_t e = prox::setup_linear4(L);
   if (e == cudaSuccess) e = dev_alloc(&L->codes, code_bytes + scale_bytes);
   if (e != cudaSuccess) {

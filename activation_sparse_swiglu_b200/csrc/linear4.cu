@@ -3,29 +3,43 @@
 //   y[b, n] = sum_g S[g, n] sum_{k in g} q[k, n] x[b, k],   q = code - 8.
 //
 // The product runs on the tensor cores with the channels as the M dimension
-// (A = the codes, widened in registers, 16 channels x 16 input rows) and the
-// tokens as N = 8 columns (B = x from shared memory), because at N = 8 the
-// fragment of a code word feeds one instruction whatever the batch: the codes,
-// which are all of the traffic, are decoded once.  Codes are stored in
-// fragment order, so a lane's 8 words of a 16 x 128 unit are two 16-byte loads
-// of a stretch that the warp reads contiguously, and no shuffle or shared
-// memory stands between HBM and the tensor core.
+// (A = the codes, 16 channels x 16 input rows) and the tokens as N = 8 columns
+// (B = x from shared memory), because at N = 8 the fragment of a code word
+// feeds one instruction whatever the batch: the codes, which are all of the
+// traffic, are decoded once.  Codes are stored in fragment order, so a lane's 8
+// words of a 16 x 128 unit are two 16-byte loads of a stretch that the warp
+// reads contiguously, and no shuffle or shared memory stands between HBM and
+// the tensor core.
 //
-// x is held in fp16: fp16 as it is; bf16 exactly, scaled by a power of two per
-// token and group; fp32 as hi + lo columns (22 significant bits) scaled the
-// same way.  A unit's sum over its 128 rows is taken by the tensor core in
-// fp32, then scaled and added in fp32, so no sum is held in fewer bits and the
-// tensor core's running sum is never longer than 8 instructions.
+// A nibble masked out of a code word is an fp16 subnormal, n 2^-24 or 16 n
+// 2^-24, so a code costs 5/8 of an instruction: x takes the factor 1/16 where
+// the nibble lies 4 bits higher, and the sum starts from -8 sum_k x, which
+// makes n the code q.  (Widening to exact integers q takes 9/8 instructions;
+// the 16-token head then ran at 0.49 of the copy bandwidth, bound by issue.)
+// The offset costs accuracy only at the level of the fp32 sums: products of up
+// to 15 |x| cancel to 7 |x|.
 //
-// Split: the units (tile of channels, group) of a cluster's tiles are dealt
-// to the CTA's warps as equal contiguous ranges; a tile that two warps share
-// is joined through shared memory in warp order, and the CTAs of a cluster
-// (which split K when there are too few channels to fill the device) join
-// theirs through distributed shared memory in rank order, so results do not
-// depend on timing and no scratch in global memory is shared between calls.
+// x is held in fp16, scaled by a power of two per token and group of 128 that
+// brings the group's largest magnitude to 2^14: fp16 and bf16 values keep all
+// their bits down to 2^-25 of that (below it, an absolute 2^-38), fp32 values
+// are split into hi + lo columns (22 significant bits).  A unit's sum over its
+// 128 rows is taken by the tensor core in fp32, then scaled and added in fp32,
+// so no sum is held in fewer bits and the tensor core's running sum is never
+// longer than 8 instructions.
+//
+// Split: the unit is one group of 128 input rows of a strip of 32 channels
+// (2 KB; two tiles, so that a fragment of x read from shared memory serves
+// two products).  The units of a cluster's strips are dealt to a CTA's warps as
+// equal contiguous ranges; a strip that several warps share is joined through
+// shared memory in warp order, and the CTAs of a cluster (which split K when
+// there are too few channels to fill the device) join theirs through
+// distributed shared memory in rank order, so results do not depend on timing
+// and no scratch in global memory is shared between calls.
 //
 // Bound: HBM at large sizes (0.52 bytes per weight), launch and one pass of
 // load latency at small ones.
+#include <cstring>
+
 #include "decode4.h"
 #include "quant4.cuh"
 
@@ -34,25 +48,30 @@ namespace {
 
 using namespace q4;
 
-constexpr int kWarps = 16;
+constexpr int kWarps = 8;
 constexpr int kThreads = kWarps * 32;
-constexpr int kXPad = 64;          // bytes; makes 16-byte reads of 8 columns conflict-free
+constexpr int kStrip = 32;                // channels of a strip
+constexpr int kXPad = 64;                 // bytes; makes 16-byte reads of 8 columns conflict-free
+constexpr int kCodeBytes = kStrip * 64;   // codes of a unit
+constexpr int kScaleBytes = kStrip * 2;   // its scales
+constexpr int kSlotBytes = kCodeBytes + 256;  // in a ring: codes, and per lane its four scales
 constexpr int kSmemLimit = 227 * 1024;
 
 struct LinearArgs {
-  const uint8_t* codes;
-  const __half* scales;
+  const char* codes;
+  const char* scales;
   const void* x;
   int64_t x_stride;
   void* out;
   int64_t out_stride;
   int B, N, G;
-  int strips;      // strips of M tiles in all
+  int strips;
   int per_clus;    // strips of a cluster
   int per_rank;    // groups of a CTA of the cluster
   int per_phase;   // groups whose x is in shared memory at once
   int cluster;
-  int x_vec;       // x rows allow 4-value vector loads
+  int ring_at;     // offset of the warps' rings in shared memory
+  int x_vec;       // x allows 16-byte loads
 };
 
 __device__ __forceinline__ uint32_t cluster_rank() {
@@ -73,20 +92,41 @@ __device__ __forceinline__ float ld_peer(const float* p, uint32_t rank) {
   return v;
 }
 
+// 0, known only once v is.
+__device__ __forceinline__ uint32_t after(uint32_t v) {
+  uint32_t r;
+  asm volatile("and.b32 %0, %1, 0;" : "=r"(r) : "r"(v));
+  return r;
+}
+
 // Start of the w-th of W equal contiguous ranges of U units.
 __device__ __forceinline__ int range_at(int U, int w, int W) { return (int)((long long)U * w / W); }
 // The range that holds unit u.
 __device__ __forceinline__ int range_of(int U, int u, int W) { return (int)(((long long)(u + 1) * W - 1) / U); }
 
-// NT column tiles of 8 (tokens, or their hi / lo parts), M tiles of 16
-// channels per strip, PF units in flight per warp.
-template <int DT, int NT, int M, int PF>
+// Eight values of x, y = v f with a further 1/16 where the codes' nibbles lie 4
+// bits higher (k mod 4 >= 2), as fp16 pairs; PARTS == 2: lo = what hi leaves.
+template <int DT>
+__device__ __forceinline__ float top8(const uint4& u) {  // largest magnitude
+  if constexpr (DT == PROX_F16) {
+    const __half2 m = __hmax2(__hmax2(__habs2(bits_h2(u.x)), __habs2(bits_h2(u.y))),
+                              __hmax2(__habs2(bits_h2(u.z)), __habs2(bits_h2(u.w))));
+    return __half2float(__hmax(__low2half(m), __high2half(m)));
+  } else {
+    // magnitudes of bf16 order like the integers of their bits
+    uint32_t m = __vmaxu2(__vmaxu2(u.x & 0x7FFF7FFFu, u.y & 0x7FFF7FFFu), __vmaxu2(u.z & 0x7FFF7FFFu, u.w & 0x7FFF7FFFu));
+    return __uint_as_float(max(m & 0xFFFFu, m >> 16) << 16);
+  }
+}
+
+// NT column tiles of 8 (tokens, or their hi / lo parts), PF units in flight
+// per warp.
+template <int DT, int NT, int PF>
 __global__ void __launch_bounds__(kThreads, 1) linear4_kernel(const LinearArgs a) {
   using T = typename Act<DT>::T;
   constexpr int PARTS = DT == PROX_F32 ? 2 : 1;
-  constexpr bool NORM = DT != PROX_F16;
+  constexpr int NC = 2 / PARTS;       // tokens of a thread per column tile
   constexpr int TB = 8 * NT / PARTS;  // tokens
-  constexpr int ROWS = 16 * M;        // channels of a strip
   extern __shared__ __align__(16) char smem[];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int g = lane >> 2, t = lane & 3;
@@ -97,34 +137,39 @@ __global__ void __launch_bounds__(kThreads, 1) linear4_kernel(const LinearArgs a
   const int cols = a.B * PARTS;
   const int xs = a.per_phase * 256 + kXPad;  // bytes of a column
   char* s_x = smem;
-  float* s_nf = reinterpret_cast<float*>(smem + (size_t)cols * xs);          // [per_phase][TB]
-  float* s_slot = s_nf + (NORM ? a.per_phase * TB : 0);                      // [kWarps][2][ROWS][B]
-  float* s_res = s_slot + kWarps * 2 * ROWS * a.B;                           // [per_clus][ROWS][B]
-  const bool use_res = a.cluster > 1 || a.per_phase < g1 - g0 || a.per_phase < a.per_rank;
+  // per group and token: 1 / the power of two, and the sum's start value
+  float2* s_nf = reinterpret_cast<float2*>(smem + (size_t)cols * xs);        // [per_phase][TB]
+  // the part of a strip that began in the warp before; a strip that goes on in
+  // the next one is left in the warp's own ring, which is idle by then
+  float* s_head = reinterpret_cast<float*>(s_nf + a.per_phase * TB);         // [kWarps][kStrip][B]
+  float* s_res = s_head + kWarps * kStrip * a.B;                             // [per_clus][kStrip][B]
+  // the warp's ring of PF units: this lane's 16 bytes of each row of codes, and
+  // its scales
+  char* ring_base = smem + a.ring_at;
+  const uint32_t ring = smem_u32(ring_base) + warp * (PF * kSlotBytes) + lane * 16;
+  const bool use_res = a.cluster > 1 || a.per_phase < a.per_rank;
   T* out = static_cast<T*>(a.out);
 
-  // A warp's results of one strip (token columns in the caller's order).
-  float acc[M][NT][4];
+  // A warp's results of one strip.
+  float acc[2][NT][2][NC];
   auto each = [&](auto&& f) {
 #pragma unroll
-    for (int m = 0; m < M; ++m)
+    for (int m = 0; m < 2; ++m)
 #pragma unroll
       for (int n = 0; n < NT; ++n)
 #pragma unroll
-        for (int r = 0; r < 2; ++r) {
-          const int row = 16 * m + 8 * r + g;
-          if (PARTS == 2) {
-            if (4 * n + t < a.B) f(row, 4 * n + t, acc[m][n][2 * r] + acc[m][n][2 * r + 1]);
-          } else {
-            if (8 * n + 2 * t < a.B) f(row, 8 * n + 2 * t, acc[m][n][2 * r]);
-            if (8 * n + 2 * t + 1 < a.B) f(row, 8 * n + 2 * t + 1, acc[m][n][2 * r + 1]);
+        for (int r = 0; r < 2; ++r)
+#pragma unroll
+          for (int e = 0; e < NC; ++e) {
+            const int b = PARTS == 2 ? 4 * n + t : 8 * n + 2 * t + e;
+            if (b < a.B) f(16 * m + 8 * r + g, b, acc[m][n][r][e]);
           }
-        }
   };
   auto put = [&](int strip, int row, int b, float v) {
-    const int n = strip * ROWS + row;
+    const int n = strip * kStrip + row;
     if (n < a.N) out[b * a.out_stride + n] = Act<DT>::from(v);
   };
+  auto tail = [&](int w) { return reinterpret_cast<float*>(ring_base + (size_t)w * (PF * kSlotBytes)); };
 
   const int phases = max(1, (a.per_rank + a.per_phase - 1) / a.per_phase);
   for (int ph = 0; ph < phases; ++ph) {
@@ -132,164 +177,248 @@ __global__ void __launch_bounds__(kThreads, 1) linear4_kernel(const LinearArgs a
     const int nG = pg1 - pg0, U = (s1 - s0) * nG;
     const int W = min(U, kWarps);
     const int beg = warp < W ? range_at(U, warp, W) : U, end = warp < W ? range_at(U, warp + 1, W) : U;
+    if (ph > 0) __syncthreads();  // x and the parts of the phase before have been read
 
-    uint4 buf[PF][M][2];
-    __half2 sc[PF][M];
-    int ls = nG ? s0 + beg / nG : 0, lg = nG ? beg % nG : 0;  // the next unit to load
-    auto load = [&](int j) {
+    // Every lane copies the very bytes it will read, so its own wait is all the
+    // synchronisation there is.  A strip's units are consecutive, and so are
+    // the strips where the CTA has all groups.
+    int strip = nG ? s0 + beg / nG : 0, gr0 = nG ? beg % nG : 0;
+    int lg = gr0;  // the next unit to load
+    const char* lp = a.codes + ((size_t)strip * a.G + pg0 + lg) * kCodeBytes + lane * 16;
+    const char* lsp = a.scales + ((size_t)strip * a.G + pg0 + lg) * kScaleBytes + g * 8;
+    int left = end - beg;
+    auto load = [&](uint32_t slot) {
+      if (left > 0) {
+        --left;
 #pragma unroll
-      for (int m = 0; m < M; ++m) {
-        const size_t unit = (size_t)(ls * M + m) * a.G + (pg0 + lg);
-        const uint4* p = reinterpret_cast<const uint4*>(a.codes) + unit * 64 + lane;
-        buf[j][m][0] = ld_stream_v4(p);
-        buf[j][m][1] = ld_stream_v4(p + 32);
-        sc[j][m] = *(reinterpret_cast<const __half2*>(a.scales) + unit * 8 + g);
+        for (int i = 0; i < 4; ++i) cp_async16(slot + 512 * i, lp + 512 * i);
+        cp_async8(slot - lane * 8 + kCodeBytes, lsp);
+        lp += kCodeBytes;
+        lsp += kScaleBytes;
+        if (++lg == nG) {
+          lg = 0;
+          lp += (size_t)(a.G - nG) * kCodeBytes;
+          lsp += (size_t)(a.G - nG) * kScaleBytes;
+        }
       }
-      if (++lg == nG) lg = 0, ++ls;
+      cp_async_commit();
     };
     // The weights do not depend on the kernel before this one in the stream.
 #pragma unroll
-    for (int j = 0; j < PF; ++j)
-      if (beg + j < end) load(j);
+    for (int j = 0; j < PF; ++j) load(ring + j * kSlotBytes);
     if (ph == 0) {
       pdl_wait();
       pdl_trigger();
-    } else {
-      __syncthreads();  // the phase before has been read
     }
 
-    // x of this phase's groups into columns: a warp takes a token's group, XB
-    // of them at once so that their loads overlap.
+    // x of this phase's groups into columns: half a warp takes a token's group,
+    // a warp XB pairs of groups at once so that their loads overlap.
     constexpr int XB = 4;
-    for (int first = warp; first < a.B * nG; first += XB * kWarps) {
-      float v[XB][4];
+    const int pairs = (nG + 1) / 2;
+    for (int first = warp; first < a.B * pairs; first += XB * kWarps) {
+      constexpr int Q = DT == PROX_F32 ? 2 : 1;
+      uint4 raw[XB][Q];
 #pragma unroll
       for (int q = 0; q < XB; ++q) {
-        const int item = first + q * kWarps;
-        if (item >= a.B * nG) break;
-        const T* src = static_cast<const T*>(a.x) + (item / nG) * a.x_stride +
-                       (int64_t)(pg0 + item % nG) * kGroupRows + 4 * lane;
-        load_vals<DT, 4>(src, a.x_vec, v[q]);
+        const int item = first + q * kWarps, gr = 2 * (item % pairs) + (lane >> 4);
+        if (item >= a.B * pairs) break;
+        const T* src = static_cast<const T*>(a.x) + (item / pairs) * a.x_stride + (int64_t)(pg0 + gr) * kGroupRows +
+                       8 * (lane & 15);
+#pragma unroll
+        for (int i = 0; i < Q; ++i) raw[q][i] = make_uint4(0, 0, 0, 0);
+        if (gr < nG) {
+          if (a.x_vec) {
+#pragma unroll
+            for (int i = 0; i < Q; ++i) raw[q][i] = reinterpret_cast<const uint4*>(src)[i];
+          } else {
+            T v[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) v[i] = src[i];
+            memcpy(raw[q], v, sizeof(v));
+          }
+        }
       }
 #pragma unroll
       for (int q = 0; q < XB; ++q) {
-        const int item = first + q * kWarps;
-        if (item >= a.B * nG) break;
-        const int b = item / nG, gr = item % nG;
-        float f = 1.f;
-        if (NORM) {
-          float mx = fmaxf(fmaxf(fabsf(v[q][0]), fabsf(v[q][1])), fmaxf(fabsf(v[q][2]), fabsf(v[q][3])));
-#pragma unroll
-          for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
-          f = normaliser(mx);
-          if (lane == 0) s_nf[gr * TB + b] = inv_pow2(f);
+        const int item = first + q * kWarps, gr = 2 * (item % pairs) + (lane >> 4), b = item / pairs;
+        if (item >= a.B * pairs) break;
+        float mx;
+        if constexpr (DT == PROX_F32) {
+          const uint4 u = raw[q][0], w = raw[q][1];
+          // magnitudes order like the integers of their bits (NaN above all)
+          const uint32_t m = max(max(max(u.x & 0x7FFFFFFFu, u.y & 0x7FFFFFFFu), max(u.z & 0x7FFFFFFFu, u.w & 0x7FFFFFFFu)),
+                                 max(max(w.x & 0x7FFFFFFFu, w.y & 0x7FFFFFFFu), max(w.z & 0x7FFFFFFFu, w.w & 0x7FFFFFFFu)));
+          mx = __uint_as_float(m);
+        } else {
+          mx = top8<DT>(raw[q][0]);
         }
-        float hi[4], lo[4];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const float y = v[q][i] * f;
-          hi[i] = __half2float(__float2half_rn(y));
-          lo[i] = y - hi[i];
+        for (int o = 8; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+        const float f = normaliser(mx);
+        if (gr < nG) {
+          uint32_t hi[4], lo[4] = {};
+          if constexpr (DT == PROX_F32) {
+            float v[8];
+            memcpy(v, raw[q], sizeof(v));
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              const float k = i & 1 ? 0.0625f * f : f;
+              const float y0 = v[2 * i] * k, y1 = v[2 * i + 1] * k;
+              const __half2 h = __floats2half2_rn(y0, y1);
+              const float2 back = __half22float2(h);
+              hi[i] = h2_bits(h);
+              lo[i] = h2_bits(__floats2half2_rn(y0 - back.x, y1 - back.y));
+            }
+          } else {
+            const uint32_t w[4] = {raw[q][0].x, raw[q][0].y, raw[q][0].z, raw[q][0].w};
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              const float k = i & 1 ? 0.0625f * f : f;
+              const float2 v = DT == PROX_F16 ? __half22float2(bits_h2(w[i])) : bf16x2_to_f2(w[i]);
+              hi[i] = h2_bits(__floats2half2_rn(v.x * k, v.y * k));
+            }
+          }
+          char* col = s_x + (size_t)(b * PARTS) * xs + gr * 256 + 16 * (lane & 15);
+          *reinterpret_cast<uint4*>(col) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+          if (PARTS == 2) *reinterpret_cast<uint4*>(col + xs) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+          if ((lane & 15) == 0) s_nf[gr * TB + b].x = inv_pow2(f);
         }
-        char* col = s_x + (size_t)(b * PARTS) * xs + gr * 256 + 8 * lane;
-        store_vals<PROX_F16, 4>(reinterpret_cast<__half*>(col), true, hi);
-        if (PARTS == 2) store_vals<PROX_F16, 4>(reinterpret_cast<__half*>(col + xs), true, lo);
       }
     }
     __syncthreads();
 
     // this lane's column of x in each tile (columns past the batch repeat the
     // last one; their results are not used)
-    const char* xcol[NT];
+    uint32_t xcol[NT];
 #pragma unroll
-    for (int n = 0; n < NT; ++n) xcol[n] = s_x + (size_t)min(8 * n + g, cols - 1) * xs + 16 * t;
-    const float* nf = s_nf + (PARTS == 2 ? t : 2 * t);
-
-    auto flush = [&](int strip) {
-      const int from = (strip - s0) * nG;  // the strip's units: [from, from + nG)
-      if (from >= beg && from + nG <= end) {
-        if (!use_res)
-          each([&](int row, int b, float v) { put(strip, row, b, v); });
-        else
-          each([&](int row, int b, float v) {
-            float* r = s_res + ((size_t)(strip - s0) * ROWS + row) * a.B + b;
-            *r = ph == 0 ? v : *r + v;
-          });
-      } else {
-        float* slot = s_slot + (size_t)(warp * 2 + (from < beg ? 0 : 1)) * ROWS * a.B;
-        each([&](int row, int b, float v) { slot[row * a.B + b] = v; });
+    for (int n = 0; n < NT; ++n) xcol[n] = smem_u32(s_x) + min(8 * n + g, cols - 1) * xs + 16 * t;
+    // start values: -8 sum_k x, by the same product with the code 8 everywhere
+    for (int gr = warp; gr < nG; gr += kWarps)
+#pragma unroll
+      for (int n = 0; n < NT; ++n) {
+        float d[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const uint4 xv = lds128(xcol[n] + gr * 256 + i * 64);
+          mma_f16(d, 0x00080008u, 0x00080008u, 0x00800080u, 0x00800080u, xv.x, xv.y);
+          mma_f16(d, 0x00080008u, 0x00080008u, 0x00800080u, 0x00800080u, xv.z, xv.w);
+        }
+        if (g == 0) {
+          float2* nf = s_nf + gr * TB;
+          if (PARTS == 2) {
+            nf[4 * n + t].y = -(d[0] + d[1]);
+          } else {
+            nf[8 * n + 2 * t].y = -d[0];
+            nf[8 * n + 2 * t + 1].y = -d[1];
+          }
+        }
       }
-    };
-    auto clear = [&]() {
+    __syncthreads();
+    const uint32_t nf0 = smem_u32(s_nf + NC * t);
+
+    uint32_t slot = ring;
+    for (int u = beg; u < end;) {
+      const int n_units = min(nG - gr0, end - u);  // of this strip
 #pragma unroll
-      for (int m = 0; m < M; ++m)
+      for (int m = 0; m < 2; ++m)
 #pragma unroll
         for (int n = 0; n < NT; ++n)
 #pragma unroll
-          for (int i = 0; i < 4; ++i) acc[m][n][i] = 0.f;
-    };
-
-    clear();
-    int cs = nG ? s0 + beg / nG : 0, cg = nG ? beg % nG : 0;  // the unit to compute
-    for (int base = beg; base < end; base += PF) {
+          for (int r = 0; r < 2; ++r)
 #pragma unroll
-      for (int j = 0; j < PF; ++j) {
-        if (base + j >= end) break;
-        // two chains per tile: even and odd 16-row steps
-        float part[M][NT][2][4];
+            for (int e = 0; e < NC; ++e) acc[m][n][r][e] = 0.f;
+      uint32_t xa[NT], nf = nf0 + gr0 * (TB * 8);
 #pragma unroll
-        for (int m = 0; m < M; ++m)
+      for (int n = 0; n < NT; ++n) xa[n] = xcol[n] + gr0 * 256;
+      for (int i_unit = 0; i_unit < n_units; ++i_unit) {
+        cp_async_wait<PF - 1>();
+        uint4 w[2][2];
 #pragma unroll
-          for (int n = 0; n < NT; ++n)
+        for (int m = 0; m < 2; ++m)
 #pragma unroll
-            for (int i = 0; i < 4; ++i) part[m][n][0][i] = part[m][n][1][i] = 0.f;
+          for (int h = 0; h < 2; ++h) w[m][h] = lds128(slot + (2 * m + h) * 512);
+        const uint2 scw = lds64(slot - lane * 8 + kCodeBytes);
+        float inv[NT][NC], start[NT][NC];
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+          if constexpr (PARTS == 2) {
+            const uint2 f = lds64(nf + 32 * n);
+            inv[n][0] = __uint_as_float(f.x), start[n][0] = __uint_as_float(f.y);
+          } else {
+            const uint4 f = lds128(nf + 64 * n);
+            inv[n][0] = __uint_as_float(f.x), start[n][0] = __uint_as_float(f.y);
+            inv[n][NC - 1] = __uint_as_float(f.z), start[n][NC - 1] = __uint_as_float(f.w);
+          }
+        }
+        // the copy into the slot just read starts once the reads (which come
+        // back in order) are here
+        load(slot + after(scw.y));
+        slot = slot == ring + (PF - 1) * kSlotBytes ? ring : slot + kSlotBytes;
+        float d[2][NT][4];
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           uint4 xv[NT];
 #pragma unroll
-          for (int n = 0; n < NT; ++n) xv[n] = lds_v4(xcol[n] + cg * 256 + i * 64);
+          for (int n = 0; n < NT; ++n) xv[n] = lds128(xa[n] + i * 64);
 #pragma unroll
-          for (int m = 0; m < M; ++m) {
-            const uint4 w4 = buf[j][m][i >> 1];
-            const uint32_t w0 = (i & 1) ? w4.z : w4.x, w1 = (i & 1) ? w4.w : w4.y;
+          for (int m = 0; m < 2; ++m) {
+            const uint4 w4 = w[m][i >> 1];
             uint32_t r[4];
-            widen8(w0, r);
+            spread8((i & 1) ? w4.z : w4.x, r);
 #pragma unroll
-            for (int n = 0; n < NT; ++n) mma_f16(part[m][n][0], r[0], r[2], r[1], r[3], xv[n].x, xv[n].y);
-            widen8(w1, r);
-#pragma unroll
-            for (int n = 0; n < NT; ++n) mma_f16(part[m][n][1], r[0], r[2], r[1], r[3], xv[n].z, xv[n].w);
-          }
-        }
-#pragma unroll
-        for (int n = 0; n < NT; ++n) {
-          float f0 = 1.f, f1 = 1.f;
-          if (NORM) {
-            if (PARTS == 2) {
-              f0 = f1 = nf[cg * TB + 4 * n];
-            } else {
-              const float2 f = *reinterpret_cast<const float2*>(nf + cg * TB + 8 * n);
-              f0 = f.x, f1 = f.y;
+            for (int n = 0; n < NT; ++n) {
+              if (i == 0) {
+                // the lo columns of fp32 start from zero
+                const float c0 = start[n][0], c1 = PARTS == 2 ? 0.f : start[n][NC - 1];
+                mma_f16(d[m][n], r[0], r[2], r[1], r[3], xv[n].x, xv[n].y, c0, c1, c0, c1);
+              } else {
+                mma_f16(d[m][n], r[0], r[2], r[1], r[3], xv[n].x, xv[n].y);
+              }
             }
-          }
+            spread8((i & 1) ? w4.w : w4.y, r);
 #pragma unroll
-          for (int m = 0; m < M; ++m) {
-            const float2 s = __half22float2(sc[j][m]);
-            float* p0 = part[m][n][0];
-            const float* p1 = part[m][n][1];
-            acc[m][n][0] = fmaf((p0[0] + p1[0]) * s.x, f0, acc[m][n][0]);
-            acc[m][n][1] = fmaf((p0[1] + p1[1]) * s.x, f1, acc[m][n][1]);
-            acc[m][n][2] = fmaf((p0[2] + p1[2]) * s.y, f0, acc[m][n][2]);
-            acc[m][n][3] = fmaf((p0[3] + p1[3]) * s.y, f1, acc[m][n][3]);
+            for (int n = 0; n < NT; ++n) mma_f16(d[m][n], r[0], r[2], r[1], r[3], xv[n].z, xv[n].w);
           }
         }
-        if (base + j + PF < end) load(j);
-        if (++cg == nG || base + j + 1 == end) {
-          flush(cs);
-          clear();
-          if (cg == nG) cg = 0, ++cs;
+#pragma unroll
+        for (int m = 0; m < 2; ++m) {
+          const float2 s2 = __half22float2(bits_h2(m ? scw.y : scw.x));
+          const float s[2] = {s2.x * 0x1p24f, s2.y * 0x1p24f};
+#pragma unroll
+          for (int n = 0; n < NT; ++n)
+#pragma unroll
+            for (int r = 0; r < 2; ++r)
+#pragma unroll
+              for (int e = 0; e < NC; ++e) {
+                const float z = PARTS == 2 ? d[m][n][2 * r] + d[m][n][2 * r + 1] : d[m][n][2 * r + e];
+                acc[m][n][r][e] = fmaf(z * s[r], inv[n][e], acc[m][n][r][e]);
+              }
         }
+#pragma unroll
+        for (int n = 0; n < NT; ++n) xa[n] += 256;
+        nf += TB * 8;
       }
+      // the strip's results, or this warp's part of them
+      if (n_units == nG) {
+        if (!use_res)
+          each([&](int row, int b, float v) { put(strip, row, b, v); });
+        else
+          each([&](int row, int b, float v) {
+            float* r = s_res + ((strip - s0) * kStrip + row) * a.B + b;
+            *r = ph == 0 ? v : *r + v;
+          });
+      } else {
+        float* part = s_head + warp * kStrip * a.B;
+        if (gr0 == 0) {  // the range ends here: the ring has been read
+          cp_async_wait<0>();
+          __syncwarp();
+          part = tail(warp);
+        }
+        each([&](int row, int b, float v) { part[row * a.B + b] = v; });
+      }
+      u += n_units;
+      gr0 = 0;
+      ++strip;
     }
     __syncthreads();
     // strips that several warps share, in warp order
@@ -297,13 +426,13 @@ __global__ void __launch_bounds__(kThreads, 1) linear4_kernel(const LinearArgs a
       const int from = (s - s0) * nG;
       const int wa = range_of(U, from, W), wb = range_of(U, from + nG - 1, W);
       if (wa == wb) continue;
-      for (int e = lane; e < ROWS * a.B; e += 32) {
+      for (int e = lane; e < kStrip * a.B; e += 32) {
         // e runs over the rows of one token first: neighbours in the output
-        const int b = e / ROWS, row = e % ROWS;
-        float v = s_slot[(size_t)(wa * 2 + 1) * ROWS * a.B + row * a.B + b];
-        for (int w = wa + 1; w <= wb; ++w) v += s_slot[(size_t)(w * 2) * ROWS * a.B + row * a.B + b];
+        const int b = e / kStrip, row = e % kStrip;
+        float v = tail(wa)[row * a.B + b];
+        for (int w = wa + 1; w <= wb; ++w) v += s_head[(w * kStrip + row) * a.B + b];
         if (use_res) {
-          float* r = s_res + ((size_t)(s - s0) * ROWS + row) * a.B + b;
+          float* r = s_res + ((s - s0) * kStrip + row) * a.B + b;
           *r = ph == 0 ? v : *r + v;
         } else {
           put(s, row, b, v);
@@ -319,10 +448,10 @@ __global__ void __launch_bounds__(kThreads, 1) linear4_kernel(const LinearArgs a
   // the cluster's CTAs share out the results; ranks are added in order (a rank
   // without groups holds none)
   const int ranks = min(a.cluster, (a.G + a.per_rank - 1) / a.per_rank);
-  const int E = (s1 - s0) * ROWS * a.B;
+  const int E = (s1 - s0) * kStrip * a.B;
   for (int e = rank * kThreads + threadIdx.x; e < E; e += a.cluster * kThreads) {
-    const int s = e / (ROWS * a.B), b = e / ROWS % a.B, row = e % ROWS;
-    const float* p = s_res + ((size_t)s * ROWS + row) * a.B + b;
+    const int row = e % kStrip, b = e / kStrip % a.B, s = e / (kStrip * a.B);
+    const float* p = s_res + (s * kStrip + row) * a.B + b;
     float v = a.cluster > 1 ? ld_peer(p, 0) : *p;
     for (int r = 1; r < ranks; ++r) v += ld_peer(p, r);
     put(s0 + s, row, b, v);
@@ -330,23 +459,25 @@ __global__ void __launch_bounds__(kThreads, 1) linear4_kernel(const LinearArgs a
   if (a.cluster > 1) cluster_sync_all();  // no CTA leaves while its results are read
 }
 
-// Word j of lane l of unit (tile, g): see widen8's order; rows past N hold
-// zeros with scale 0.
+// codes [strips][G][4][32 lanes][4 words]: row h of tile m (index 2 m + h) holds
+// the steps 2h and 2h + 1 of 32 input rows; word wi of a row: see spread8's
+// order.  scales [strips][G][8][tile][2].  Channels past N hold code 8 and
+// scale 0.
 __global__ void linear4_pack_kernel(const uint8_t* __restrict__ codes, const __half* __restrict__ scales, int N, int G,
-                                    int S, uint32_t* __restrict__ out, __half* __restrict__ out_scales) {
-  const size_t n_word = (size_t)S * G * 256, n_scale = (size_t)S * G * 16;
+                                    int strips, uint32_t* __restrict__ out, __half* __restrict__ out_scales) {
+  const size_t n_word = (size_t)strips * G * (kCodeBytes / 4), n_scale = (size_t)strips * G * kStrip;
   const size_t stride = (size_t)gridDim.x * blockDim.x;
   for (size_t i = (size_t)blockIdx.x * blockDim.x + threadIdx.x; i < n_word + n_scale; i += stride) {
     if (i < n_word) {
-      const int wi = i & 3, l = (i >> 2) & 31, j = (i >> 7) & 1;
-      const size_t unit = i >> 8;
-      const int gr = unit % G, tile = unit / G;
-      const int k0 = gr * kGroupRows + 32 * (2 * j + (wi >> 1)) + 8 * (l & 3) + 4 * (wi & 1);
+      const int wi = i & 3, l = (i >> 2) & 31, h = (i >> 7) & 1, m = (i >> 8) & 1;
+      const size_t unit = i >> 9;
+      const int gr = unit % G, strip = unit / G;
+      const int k0 = gr * kGroupRows + 32 * (2 * h + (wi >> 1)) + 8 * (l & 3) + 4 * (wi & 1);
       uint32_t w = 0;
 #pragma unroll
       for (int nib = 0; nib < 8; ++nib) {
         // nibbles 0, 4, 1, 5: row l / 4, input rows k0 .. k0 + 3; 2, 6, 3, 7: row + 8
-        const int n = tile * 16 + (l >> 2) + ((nib & 2) ? 8 : 0);
+        const int n = strip * kStrip + 16 * m + (l >> 2) + ((nib & 2) ? 8 : 0);
         const int k = k0 + 2 * (nib & 1) + (nib >> 2);
         const uint32_t c = n < N ? (codes[(size_t)k * (N / 2) + n / 2] >> (4 * (n & 1))) & 15u : 8u;
         w |= c << (4 * nib);
@@ -354,10 +485,10 @@ __global__ void linear4_pack_kernel(const uint8_t* __restrict__ codes, const __h
       out[i] = w;
     } else {
       const size_t u = i - n_word;
-      const int r = u & 15;
-      const size_t unit = u >> 4;
-      const int gr = unit % G, tile = unit / G;
-      const int n = tile * 16 + (r >> 1) + 8 * (r & 1);
+      const int r = u & 1, m = (u >> 1) & 1, gq = (u >> 2) & 7;
+      const size_t unit = u >> 5;
+      const int gr = unit % G, strip = unit / G;
+      const int n = strip * kStrip + 16 * m + 8 * r + gq;
       out_scales[u] = n < N ? scales[(size_t)gr * N + n] : __half(0.f);
     }
   }
@@ -370,61 +501,60 @@ int col_tiles(int B, int dtype) {
   const int cols = dtype == PROX_F32 ? 2 * B : B;
   return cols <= 8 ? 1 : cols <= 16 ? 2 : 4;
 }
-// One tile of channels per strip up to 16 columns.  At 32 columns the x reads
-// from shared memory would take longer than the codes from HBM, so two tiles
-// share them.
-int strip_tiles(int nt) { return nt == 4 ? 2 : 1; }
 
-Kernel pick(int dtype, int nt) {
+// Units in flight per warp: 8 cover a small matrix's whole share at once; 4 or
+// 2 where x takes the room.
+template <int PF>
+Kernel pick_depth(int dtype, int nt) {
   switch (dtype) {
     case PROX_F32:
-      return nt == 1 ? linear4_kernel<PROX_F32, 1, 1, 4>
-                     : nt == 2 ? linear4_kernel<PROX_F32, 2, 1, 4> : linear4_kernel<PROX_F32, 4, 2, 1>;
-    case PROX_F16: return nt == 1 ? linear4_kernel<PROX_F16, 1, 1, 4> : linear4_kernel<PROX_F16, 2, 1, 4>;
-    default: return nt == 1 ? linear4_kernel<PROX_BF16, 1, 1, 4> : linear4_kernel<PROX_BF16, 2, 1, 4>;
+      return nt == 1 ? linear4_kernel<PROX_F32, 1, PF>
+                     : nt == 2 ? linear4_kernel<PROX_F32, 2, PF> : linear4_kernel<PROX_F32, 4, PF>;
+    case PROX_F16: return nt == 1 ? linear4_kernel<PROX_F16, 1, PF> : linear4_kernel<PROX_F16, 2, PF>;
+    default: return nt == 1 ? linear4_kernel<PROX_BF16, 1, PF> : linear4_kernel<PROX_BF16, 2, PF>;
   }
+}
+Kernel pick(int dtype, int nt, int depth) {
+  return depth == 8 ? pick_depth<8>(dtype, nt) : depth == 4 ? pick_depth<4>(dtype, nt) : pick_depth<2>(dtype, nt);
 }
 
 struct Plan {
-  int cluster, per_clus, per_rank, per_phase, clusters;
-  size_t smem;
+  int cluster, per_clus, per_rank, per_phase, clusters, depth;
+  size_t ring_at, smem;
 };
 
-size_t smem_bytes(int cols, int B, int tb, bool norm, int rows, int per_phase, int res_strips) {
-  return (size_t)cols * (per_phase * 256 + kXPad) + (norm ? (size_t)per_phase * tb * 4 : 0) +
-         (size_t)(kWarps * 2 + res_strips) * rows * B * 4;
-}
+size_t ring_bytes(int depth) { return (size_t)kWarps * depth * kSlotBytes; }
 
-// The cluster size whose busiest warp has the least to do.  Counted in units
-// of one warp (a 16 x 128 block of codes, about 1 KB): a CTA's units over its
-// 16 warps, plus what joining across the cluster costs (about 1 us, what 40
-// units of the CTA take), plus a penalty per extra phase of x.
+// The cluster size whose busiest CTA has the least to do: its units (2 KB of
+// codes each, about 90 SM cycles at the copy bandwidth), plus what joining
+// across the cluster costs (about 1 us, 20 units), plus 30 per extra phase of
+// x (the rings run dry and x is converted again).
 bool plan_linear4(const prox_linear4* L, int B, int dtype, Plan* best) {
-  const int nt = col_tiles(B, dtype), M = strip_tiles(nt), parts = dtype == PROX_F32 ? 2 : 1;
-  const int rows = 16 * M, cols = B * parts, tb = 8 * nt / parts;
-  const int strips = (L->S + M - 1) / M;
+  const int nt = col_tiles(B, dtype), parts = dtype == PROX_F32 ? 2 : 1;
+  const int cols = B * parts, tb = 8 * nt / parts;
   double least = 1e300;
   for (int ci = 0; ci < 4; ++ci) {
     const int c = 1 << ci;
     if (L->clusters[ci] < 1 || (c > 1 && c > L->G)) continue;
     Plan p;
     p.cluster = c;
-    p.clusters = strips < L->clusters[ci] ? strips : L->clusters[ci];
-    p.per_clus = (strips + p.clusters - 1) / p.clusters;
-    p.clusters = (strips + p.per_clus - 1) / p.per_clus;
+    p.clusters = L->strips < L->clusters[ci] ? L->strips : L->clusters[ci];
+    p.per_clus = (L->strips + p.clusters - 1) / p.clusters;
+    p.clusters = (L->strips + p.per_clus - 1) / p.per_clus;
     p.per_rank = (L->G + c - 1) / c;
     p.per_phase = p.per_rank;
-    const bool norm = dtype != PROX_F16;
-    while (smem_bytes(cols, B, tb, norm, rows, p.per_phase,
-                      c > 1 || p.per_phase < p.per_rank ? p.per_clus : 0) > kSmemLimit) {
-      if (p.per_phase == 1) break;
-      p.per_phase = (p.per_phase + 1) / 2;
-    }
-    p.smem = smem_bytes(cols, B, tb, norm, rows, p.per_phase,
-                        c > 1 || p.per_phase < p.per_rank ? p.per_clus : 0);
-    if (p.smem > kSmemLimit) continue;
+    auto front = [&] {  // everything before the rings
+      const int res = c > 1 || p.per_phase < p.per_rank ? p.per_clus : 0;
+      return ((size_t)cols * (p.per_phase * 256 + kXPad) + (size_t)p.per_phase * tb * 8 +
+              (size_t)(kWarps + res) * kStrip * B * 4 + 15) & ~(size_t)15;
+    };
+    while (front() + ring_bytes(2) > kSmemLimit && p.per_phase > 1) p.per_phase = (p.per_phase + 1) / 2;
+    p.ring_at = front();
+    if (p.ring_at + ring_bytes(2) > kSmemLimit) continue;
+    p.depth = p.ring_at + ring_bytes(8) <= kSmemLimit ? 8 : p.ring_at + ring_bytes(4) <= kSmemLimit ? 4 : 2;
+    p.smem = p.ring_at + ring_bytes(p.depth);
     const int phases = (p.per_rank + p.per_phase - 1) / p.per_phase;
-    const double cost = (double)p.per_clus * M * p.per_rank + (c > 1 ? 40.0 : 0.0) + 60.0 * (phases - 1);
+    const double cost = (double)p.per_clus * p.per_rank + (c > 1 ? 20.0 : 0.0) + 30.0 * (phases - 1);
     if (cost < least) {
       least = cost;
       *best = p;
@@ -436,7 +566,7 @@ bool plan_linear4(const prox_linear4* L, int B, int dtype, Plan* best) {
 }  // namespace
 
 cudaError_t launch_linear4_pack(const uint8_t* codes, const uint16_t* scales, const prox_linear4* L, cudaStream_t s) {
-  linear4_pack_kernel<<<1184, 256, 0, s>>>(codes, reinterpret_cast<const __half*>(scales), L->N, L->G, L->S,
+  linear4_pack_kernel<<<1184, 256, 0, s>>>(codes, reinterpret_cast<const __half*>(scales), L->N, L->G, L->strips,
                                            reinterpret_cast<uint32_t*>(L->codes),
                                            reinterpret_cast<__half*>(L->scales));
   return cudaGetLastError();
@@ -446,9 +576,11 @@ cudaError_t setup_linear4(prox_linear4* L) {
   for (int dtype : {PROX_F32, PROX_F16, PROX_BF16})
     for (int nt : {1, 2, 4}) {
       if (nt == 4 && dtype != PROX_F32) continue;
-      const Kernel k = pick(dtype, nt);
-      cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemLimit);
-      if (e != cudaSuccess) return e;
+      for (int depth : {2, 4, 8}) {
+        cudaError_t e = cudaFuncSetAttribute(pick(dtype, nt, depth), cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                             kSmemLimit);
+        if (e != cudaSuccess) return e;
+      }
     }
   L->clusters[0] = L->num_sms;
   for (int ci = 1; ci < 4; ++ci) {
@@ -464,7 +596,7 @@ cudaError_t setup_linear4(prox_linear4* L) {
     cfg.attrs = attr;
     cfg.numAttrs = 1;
     int n = 0;
-    cudaError_t e = cudaOccupancyMaxActiveClusters(&n, pick(PROX_BF16, 1), &cfg);
+    cudaError_t e = cudaOccupancyMaxActiveClusters(&n, pick(PROX_BF16, 1, 4), &cfg);
     if (e != cudaSuccess) return e;
     L->clusters[ci] = n;
   }
@@ -475,10 +607,10 @@ cudaError_t launch_linear4(const prox_linear4* L, const void* x, int64_t x_strid
                            int B, int dtype, cudaStream_t s) {
   Plan p;
   if (!plan_linear4(L, B, dtype, &p)) return cudaErrorInvalidConfiguration;
-  const int nt = col_tiles(B, dtype), M = strip_tiles(nt);
+  const int nt = col_tiles(B, dtype);
   LinearArgs a;
-  a.codes = L->codes;
-  a.scales = reinterpret_cast<const __half*>(L->scales);
+  a.codes = reinterpret_cast<const char*>(L->codes);
+  a.scales = reinterpret_cast<const char*>(L->scales);
   a.x = x;
   a.x_stride = x_stride;
   a.out = out;
@@ -486,13 +618,13 @@ cudaError_t launch_linear4(const prox_linear4* L, const void* x, int64_t x_strid
   a.B = B;
   a.N = L->N;
   a.G = L->G;
-  a.strips = (L->S + M - 1) / M;
+  a.strips = L->strips;
   a.per_clus = p.per_clus;
   a.per_rank = p.per_rank;
   a.per_phase = p.per_phase;
   a.cluster = p.cluster;
-  const int bytes4 = dtype == PROX_F32 ? 16 : 8;
-  a.x_vec = (reinterpret_cast<uintptr_t>(x) % bytes4) == 0 && x_stride % 4 == 0;
+  a.ring_at = (int)p.ring_at;
+  a.x_vec = (reinterpret_cast<uintptr_t>(x) & 15) == 0 && (B == 1 || x_stride % (dtype == PROX_F32 ? 4 : 8) == 0);
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)(p.clusters * p.cluster), 1, 1);
   cfg.blockDim = dim3(kThreads, 1, 1);
@@ -507,7 +639,7 @@ cudaError_t launch_linear4(const prox_linear4* L, const void* x, int64_t x_strid
   attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = p.cluster > 1 ? 2 : 1;
-  return cudaLaunchKernelEx(&cfg, pick(dtype, nt), a);
+  return cudaLaunchKernelEx(&cfg, pick(dtype, nt, p.depth), a);
 }
 
 }  // namespace prox

@@ -45,6 +45,19 @@ __device__ __forceinline__ void widen8(uint32_t w, uint32_t (&r)[4]) {
   r[3] = widen<true>(w);
 }
 
+// The word's nibbles as fp16 subnormals: n 2^-24 in r[0] = nibbles (0, 4) and
+// r[2] = (2, 6), 16 n 2^-24 in r[1] = (1, 5) and r[3] = (3, 7).  A nibble in the
+// low mantissa bits of an fp16 zero IS that number, so this is five logical
+// instructions for eight codes; the factor 16 goes into the other operand and
+// the offset 8 into the sum's start value.
+__device__ __forceinline__ void spread8(uint32_t w, uint32_t (&r)[4]) {
+  r[0] = w & 0x000F000Fu;
+  r[1] = w & 0x00F000F0u;
+  w >>= 8;
+  r[2] = w & 0x000F000Fu;
+  r[3] = w & 0x00F000F0u;
+}
+
 // D[16 x 8] += A[16 x 16] B[16 x 8], fp16 operands, fp32 sums.
 __device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
                                         uint32_t b0, uint32_t b1) {
@@ -53,6 +66,16 @@ __device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1,
       "{%0,%1,%2,%3};"
       : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+// D = A B + C.
+__device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                        uint32_t b0, uint32_t b1, float c0, float c1, float c2, float c3) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
+      "{%10,%11,%12,%13};"
+      : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(c0), "f"(c1), "f"(c2), "f"(c3));
 }
 
 // The transpose of an 8 x 8 matrix of 16-bit values held as fragments.
@@ -75,8 +98,29 @@ __device__ __forceinline__ float max_nan(float a, float b) {
   return y;
 }
 
-__device__ __forceinline__ void cp_async16(void* dst, const void* src) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(dst)), "l"(src) : "memory");
+// ---- shared memory by 32-bit address -----------------------------------------
+// (A generic pointer costs 64-bit additions and a conversion per access; these
+// fold a constant into the instruction.)
+__device__ __forceinline__ uint4 lds128(uint32_t addr) {
+  uint4 v;
+  asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(addr));
+  return v;
+}
+__device__ __forceinline__ uint2 lds64(uint32_t addr) {
+  uint2 v;
+  asm volatile("ld.shared.v2.u32 {%0,%1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(addr));
+  return v;
+}
+__device__ __forceinline__ uint32_t lds32(uint32_t addr) {
+  uint32_t v;
+  asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v) : "r"(addr));
+  return v;
+}
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void cp_async8(uint32_t dst, const void* src) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(dst), "l"(src) : "memory");
 }
 __device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int N>

@@ -33,17 +33,23 @@ def random_codes(gen, shape, device):
 def linear4(x, codes, scales):
     """y = x W in 64 bits, and the bound on a result's error."""
     K, N = codes.shape[0], scales.shape[1]
-    w = unpack(codes).double().view(K // 128, 128, N) * scales.double()[:, None, :]
-    w = w.view(K, N)
+    q, s = unpack(codes).double().view(K // 128, 128, N), scales.double()[:, None, :]
+    w = (q * s).view(K, N)
     xd = x.double()
-    y, mag = xd @ w, xd.abs() @ w.abs()
-    # the groups' sums are added one after the other, after at most 8 tensor
-    # core steps and 3 multiplications; warps and CTAs join 16 + 8 parts; fp32
-    # inputs carry 22 bits
-    n = K // 128 + 8 + 3 + 24
+    y = xd @ w
+    # The sums run over codes q + 8 and start from -8 sum x: terms of up to
+    # (|q| + 16) |x| S.  The groups' sums are added one after the other, after
+    # at most 8 tensor core steps and 3 multiplications; warps and CTAs join
+    # 16 + 8 parts; the start value is a sum of 128 values over 7 levels.
+    mag = xd.abs() @ ((q.abs() + 16) * s.abs()).view(K, N)
+    n = K // 128 + 8 + 3 + 24 + 7
     tol = n * 2.0 ** -23 * mag + HALF_STEP[x.dtype] * y.abs()
+    # fp32 inputs carry 22 bits; what lies below 2^-25 of its group's largest
+    # magnitude has an absolute step of 2^-38 of it (2^-39 off, hi and lo)
     if x.dtype == torch.float32:
         tol = tol + 2.0 ** -22 * mag
+    top = xd.abs().view(-1, K // 128, 128).amax(-1)
+    tol = tol + 2.0 ** -38 * (top @ ((q.abs() + 16) * s.abs()).sum(1))
     if x.dtype == torch.float16:
         tol = tol + 2.0 ** -24  # below fp16's normal range a step is 2^-24
     return y, tol
