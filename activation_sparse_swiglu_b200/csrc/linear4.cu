@@ -38,8 +38,6 @@
 //
 // Bound: HBM at large sizes (0.52 bytes per weight), launch and one pass of
 // load latency at small ones.
-#include <cstring>
-
 #include "decode4.h"
 #include "quant4.cuh"
 
@@ -48,14 +46,15 @@ namespace {
 
 using namespace q4;
 
-constexpr int kWarps = 8;
-constexpr int kThreads = kWarps * 32;
+// Warps of a CTA: as many as the registers of NT column tiles allow.
+constexpr int warps_of(int nt) { return nt == 1 ? 16 : nt == 2 ? 12 : 8; }
 constexpr int kStrip = 32;                // channels of a strip
+constexpr int kPartRow = 36;              // floats of a token's results of a strip (bank-conflict-free)
 constexpr int kXPad = 64;                 // bytes; makes 16-byte reads of 8 columns conflict-free
 constexpr int kCodeBytes = kStrip * 64;   // codes of a unit
 constexpr int kScaleBytes = kStrip * 2;   // its scales
 constexpr int kSlotBytes = kCodeBytes + 256;  // in a ring: codes, and per lane its four scales
-constexpr int kSmemLimit = 227 * 1024;
+constexpr int kSmemLimit = 227 * 1024 - 128;  // (a table of the warps beside it)
 
 struct LinearArgs {
   const char* codes;
@@ -100,34 +99,49 @@ __device__ __forceinline__ uint32_t after(uint32_t v) {
 }
 
 // Start of the w-th of W equal contiguous ranges of U units.
-__device__ __forceinline__ int range_at(int U, int w, int W) { return (int)((long long)U * w / W); }
+// (A CTA has at most 2^15 strips x 2^9 groups and 16 warps: 32 bits hold it.)
+__device__ __forceinline__ int range_at(int U, int w, int W) { return (int)((unsigned)U * (unsigned)w / (unsigned)W); }
 // The range that holds unit u.
-__device__ __forceinline__ int range_of(int U, int u, int W) { return (int)(((long long)(u + 1) * W - 1) / U); }
+__device__ __forceinline__ int range_of(int U, int u, int W) {
+  return (int)(((unsigned)(u + 1) * (unsigned)W - 1) / (unsigned)U);
+}
 
-// Eight values of x, y = v f with a further 1/16 where the codes' nibbles lie 4
-// bits higher (k mod 4 >= 2), as fp16 pairs; PARTS == 2: lo = what hi leaves.
+// The largest magnitude of 16 bytes of activations.
 template <int DT>
-__device__ __forceinline__ float top8(const uint4& u) {  // largest magnitude
+__device__ __forceinline__ float top(const uint4& u) {
   if constexpr (DT == PROX_F16) {
     const __half2 m = __hmax2(__hmax2(__habs2(bits_h2(u.x)), __habs2(bits_h2(u.y))),
                               __hmax2(__habs2(bits_h2(u.z)), __habs2(bits_h2(u.w))));
     return __half2float(__hmax(__low2half(m), __high2half(m)));
+  } else if constexpr (DT == PROX_BF16) {
+    const float2 a = bf16x2_to_f2(u.x), b = bf16x2_to_f2(u.y), c = bf16x2_to_f2(u.z), d = bf16x2_to_f2(u.w);
+    return fmaxf(fmaxf(fmaxf(fabsf(a.x), fabsf(a.y)), fmaxf(fabsf(b.x), fabsf(b.y))),
+                 fmaxf(fmaxf(fabsf(c.x), fabsf(c.y)), fmaxf(fabsf(d.x), fabsf(d.y))));
   } else {
-    // magnitudes of bf16 order like the integers of their bits
-    uint32_t m = __vmaxu2(__vmaxu2(u.x & 0x7FFF7FFFu, u.y & 0x7FFF7FFFu), __vmaxu2(u.z & 0x7FFF7FFFu, u.w & 0x7FFF7FFFu));
-    return __uint_as_float(max(m & 0xFFFFu, m >> 16) << 16);
+    return fmaxf(fmaxf(fabsf(__uint_as_float(u.x)), fabsf(__uint_as_float(u.y))),
+                 fmaxf(fabsf(__uint_as_float(u.z)), fabsf(__uint_as_float(u.w))));
   }
+}
+// Two fp16 or bf16 values times a power of two `to`, as fp16 (exact above 2^-14);
+// adds them times f to *sum.
+template <int DT>
+__device__ __forceinline__ uint32_t scale2(uint32_t w, float f, float to, float* sum) {
+  const float2 v = DT == PROX_F16 ? __half22float2(bits_h2(w)) : bf16x2_to_f2(w);
+  *sum = fmaf(v.x, f, fmaf(v.y, f, *sum));
+  return h2_bits(__floats2half2_rn(v.x * to, v.y * to));
 }
 
 // NT column tiles of 8 (tokens, or their hi / lo parts), PF units in flight
 // per warp.
 template <int DT, int NT, int PF>
-__global__ void __launch_bounds__(kThreads, 1) linear4_kernel(const LinearArgs a) {
+__global__ void __launch_bounds__(warps_of(NT) * 32, 1) linear4_kernel(const LinearArgs a) {
   using T = typename Act<DT>::T;
+  constexpr int kWarps = warps_of(NT), kThreads = kWarps * 32;
   constexpr int PARTS = DT == PROX_F32 ? 2 : 1;
   constexpr int NC = 2 / PARTS;       // tokens of a thread per column tile
   constexpr int TB = 8 * NT / PARTS;  // tokens
   extern __shared__ __align__(16) char smem[];
+  __shared__ int2 s_cut[kWarps];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int g = lane >> 2, t = lane & 3;
   const int rank = a.cluster > 1 ? (int)cluster_rank() : 0;
@@ -139,10 +153,7 @@ __global__ void __launch_bounds__(kThreads, 1) linear4_kernel(const LinearArgs a
   char* s_x = smem;
   // per group and token: 1 / the power of two, and the sum's start value
   float2* s_nf = reinterpret_cast<float2*>(smem + (size_t)cols * xs);        // [per_phase][TB]
-  // the part of a strip that began in the warp before; a strip that goes on in
-  // the next one is left in the warp's own ring, which is idle by then
-  float* s_head = reinterpret_cast<float*>(s_nf + a.per_phase * TB);         // [kWarps][kStrip][B]
-  float* s_res = s_head + kWarps * kStrip * a.B;                             // [per_clus][kStrip][B]
+  float* s_res = reinterpret_cast<float*>(s_nf + a.per_phase * TB);          // [per_clus][B][kPartRow]
   // the warp's ring of PF units: this lane's 16 bytes of each row of codes, and
   // its scales
   char* ring_base = smem + a.ring_at;
@@ -150,9 +161,10 @@ __global__ void __launch_bounds__(kThreads, 1) linear4_kernel(const LinearArgs a
   const bool use_res = a.cluster > 1 || a.per_phase < a.per_rank;
   T* out = static_cast<T*>(a.out);
 
-  // A warp's results of one strip.
-  float acc[2][NT][2][NC];
-  auto each = [&](auto&& f) {
+  // A warp's results of the strip it is at, and its part of a strip that began
+  // in the warp before (few enough to stay in registers).
+  float acc[2][NT][2][NC], head_acc[2][NT][2][NC];
+  auto each = [&](const float(&v)[2][NT][2][NC], auto&& f) {
 #pragma unroll
     for (int m = 0; m < 2; ++m)
 #pragma unroll
@@ -162,14 +174,17 @@ __global__ void __launch_bounds__(kThreads, 1) linear4_kernel(const LinearArgs a
 #pragma unroll
           for (int e = 0; e < NC; ++e) {
             const int b = PARTS == 2 ? 4 * n + t : 8 * n + 2 * t + e;
-            if (b < a.B) f(16 * m + 8 * r + g, b, acc[m][n][r][e]);
+            if (b < a.B) f(16 * m + 8 * r + g, b, v[m][n][r][e]);
           }
   };
   auto put = [&](int strip, int row, int b, float v) {
     const int n = strip * kStrip + row;
     if (n < a.N) out[b * a.out_stride + n] = Act<DT>::from(v);
   };
-  auto tail = [&](int w) { return reinterpret_cast<float*>(ring_base + (size_t)w * (PF * kSlotBytes)); };
+  // The parts that a warp leaves of strips it shares: in its ring, idle by then.
+  static_assert(PF >= 2 && kLinear4MaxTokens * kPartRow * 4 <= kSlotBytes, "a ring holds two parts");
+  auto head = [&](int w) { return reinterpret_cast<float*>(ring_base + (size_t)w * (PF * kSlotBytes)); };
+  auto tail = [&](int w) { return reinterpret_cast<float*>(ring_base + (size_t)w * (PF * kSlotBytes) + kSlotBytes); };
 
   const int phases = max(1, (a.per_rank + a.per_phase - 1) / a.per_phase);
   for (int ph = 0; ph < phases; ++ph) {
@@ -178,6 +193,13 @@ __global__ void __launch_bounds__(kThreads, 1) linear4_kernel(const LinearArgs a
     const int W = min(U, kWarps);
     const int beg = warp < W ? range_at(U, warp, W) : U, end = warp < W ? range_at(U, warp + 1, W) : U;
     if (ph > 0) __syncthreads();  // x and the parts of the phase before have been read
+    if (threadIdx.x < W - 1) {
+      // the strip that starts in warp w0's range and goes on past it, and the
+      // warp that it ends in
+      const int w0 = threadIdx.x, from = range_at(U, w0 + 1, W), s = from / nG;
+      const bool cut = from != s * nG && range_at(U, w0, W) <= s * nG;
+      s_cut[w0] = make_int2(cut ? s : -1, cut ? range_of(U, s * nG + nG - 1, W) : 0);
+    }
 
     // Every lane copies the very bytes it will read, so its own wait is all the
     // synchronisation there is.  A strip's units are consecutive, and so are
@@ -211,79 +233,69 @@ __global__ void __launch_bounds__(kThreads, 1) linear4_kernel(const LinearArgs a
       pdl_trigger();
     }
 
-    // x of this phase's groups into columns: half a warp takes a token's group,
-    // a warp XB pairs of groups at once so that their loads overlap.
-    constexpr int XB = 4;
-    const int pairs = (nG + 1) / 2;
-    for (int first = warp; first < a.B * pairs; first += XB * kWarps) {
-      constexpr int Q = DT == PROX_F32 ? 2 : 1;
-      uint4 raw[XB][Q];
+    // x of this phase's groups into columns.  A lane takes 64 bytes of a group
+    // (four pieces, in an order that spreads the stores over the banks), LPG
+    // lanes a group, a warp 32 / LPG groups of a token.
+    constexpr int LPG = DT == PROX_F32 ? 8 : 4, GPW = 32 / LPG;
+    const int runs = (nG + GPW - 1) / GPW;
+    for (int b = 0, run = warp; b < a.B && runs > 0;) {
+      if (run >= runs) {
+        run -= runs;
+        ++b;
+        continue;
+      }
+      const int gr = run * GPW + lane / LPG;
+      const int turn = DT == PROX_F32 ? (lane >> 2) & 3 : (lane >> 1) & 3;
+      run += kWarps;
+      uint4 raw[4];
+      const T* src = static_cast<const T*>(a.x) + b * a.x_stride + (int64_t)(pg0 + gr) * kGroupRows +
+                     (lane % LPG) * (64 / (int)sizeof(T));
 #pragma unroll
-      for (int q = 0; q < XB; ++q) {
-        const int item = first + q * kWarps, gr = 2 * (item % pairs) + (lane >> 4);
-        if (item >= a.B * pairs) break;
-        const T* src = static_cast<const T*>(a.x) + (item / pairs) * a.x_stride + (int64_t)(pg0 + gr) * kGroupRows +
-                       8 * (lane & 15);
-#pragma unroll
-        for (int i = 0; i < Q; ++i) raw[q][i] = make_uint4(0, 0, 0, 0);
+      for (int j = 0; j < 4; ++j) {
+        const T* p = src + ((j + turn) & 3) * (16 / (int)sizeof(T));
+        raw[j] = make_uint4(0, 0, 0, 0);
         if (gr < nG) {
           if (a.x_vec) {
-#pragma unroll
-            for (int i = 0; i < Q; ++i) raw[q][i] = reinterpret_cast<const uint4*>(src)[i];
+            raw[j] = *reinterpret_cast<const uint4*>(p);
           } else {
-            T v[8];
+            T v[16 / sizeof(T)];
 #pragma unroll
-            for (int i = 0; i < 8; ++i) v[i] = src[i];
-            memcpy(raw[q], v, sizeof(v));
+            for (int i = 0; i < (int)(16 / sizeof(T)); ++i) v[i] = p[i];
+            memcpy(&raw[j], v, 16);
           }
         }
       }
+      float mx = fmaxf(fmaxf(top<DT>(raw[0]), top<DT>(raw[1])), fmaxf(top<DT>(raw[2]), top<DT>(raw[3])));
 #pragma unroll
-      for (int q = 0; q < XB; ++q) {
-        const int item = first + q * kWarps, gr = 2 * (item % pairs) + (lane >> 4), b = item / pairs;
-        if (item >= a.B * pairs) break;
-        float mx;
+      for (int o = LPG / 2; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+      if (gr >= nG) continue;
+      const float f = normaliser(mx), f16 = 0.0625f * f;
+      float sum = 0.f;  // of the group's x as the products will see it
+      char* col = s_x + (size_t)(b * PARTS) * xs + gr * 256 + (lane % LPG) * (DT == PROX_F32 ? 32 : 64);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const int piece = (j + turn) & 3;
         if constexpr (DT == PROX_F32) {
-          const uint4 u = raw[q][0], w = raw[q][1];
-          // magnitudes order like the integers of their bits (NaN above all)
-          const uint32_t m = max(max(max(u.x & 0x7FFFFFFFu, u.y & 0x7FFFFFFFu), max(u.z & 0x7FFFFFFFu, u.w & 0x7FFFFFFFu)),
-                                 max(max(w.x & 0x7FFFFFFFu, w.y & 0x7FFFFFFFu), max(w.z & 0x7FFFFFFFu, w.w & 0x7FFFFFFFu)));
-          mx = __uint_as_float(m);
+          const float y[4] = {__uint_as_float(raw[j].x) * f, __uint_as_float(raw[j].y) * f,
+                              __uint_as_float(raw[j].z) * f16, __uint_as_float(raw[j].w) * f16};
+          const __half2 h0 = __floats2half2_rn(y[0], y[1]), h1 = __floats2half2_rn(y[2], y[3]);
+          const float2 b0 = __half22float2(h0), b1 = __half22float2(h1);
+          *reinterpret_cast<uint2*>(col + 8 * piece) = make_uint2(h2_bits(h0), h2_bits(h1));
+          const __half2 l0 = __floats2half2_rn(y[0] - b0.x, y[1] - b0.y), l1 = __floats2half2_rn(y[2] - b1.x, y[3] - b1.y);
+          const float2 m0 = __half22float2(l0), m1 = __half22float2(l1);
+          *reinterpret_cast<uint2*>(col + xs + 8 * piece) = make_uint2(h2_bits(l0), h2_bits(l1));
+          sum += (b0.x + m0.x) + (b0.y + m0.y);
+          sum = fmaf((b1.x + m1.x) + (b1.y + m1.y), 16.f, sum);
         } else {
-          mx = top8<DT>(raw[q][0]);
-        }
-#pragma unroll
-        for (int o = 8; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
-        const float f = normaliser(mx);
-        if (gr < nG) {
-          uint32_t hi[4], lo[4] = {};
-          if constexpr (DT == PROX_F32) {
-            float v[8];
-            memcpy(v, raw[q], sizeof(v));
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              const float k = i & 1 ? 0.0625f * f : f;
-              const float y0 = v[2 * i] * k, y1 = v[2 * i + 1] * k;
-              const __half2 h = __floats2half2_rn(y0, y1);
-              const float2 back = __half22float2(h);
-              hi[i] = h2_bits(h);
-              lo[i] = h2_bits(__floats2half2_rn(y0 - back.x, y1 - back.y));
-            }
-          } else {
-            const uint32_t w[4] = {raw[q][0].x, raw[q][0].y, raw[q][0].z, raw[q][0].w};
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              const float k = i & 1 ? 0.0625f * f : f;
-              const float2 v = DT == PROX_F16 ? __half22float2(bits_h2(w[i])) : bf16x2_to_f2(w[i]);
-              hi[i] = h2_bits(__floats2half2_rn(v.x * k, v.y * k));
-            }
-          }
-          char* col = s_x + (size_t)(b * PARTS) * xs + gr * 256 + 16 * (lane & 15);
-          *reinterpret_cast<uint4*>(col) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-          if (PARTS == 2) *reinterpret_cast<uint4*>(col + xs) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
-          if ((lane & 15) == 0) s_nf[gr * TB + b].x = inv_pow2(f);
+          *reinterpret_cast<uint4*>(col + 16 * piece) =
+              make_uint4(scale2<DT>(raw[j].x, f, f, &sum), scale2<DT>(raw[j].y, f, f16, &sum),
+                         scale2<DT>(raw[j].z, f, f, &sum), scale2<DT>(raw[j].w, f, f16, &sum));
         }
       }
+      const unsigned mask = (LPG == 8 ? 0xFFu : 0xFu) << (lane / LPG * LPG);
+#pragma unroll
+      for (int o = LPG / 2; o > 0; o >>= 1) sum += __shfl_xor_sync(mask, sum, o);
+      if (lane % LPG == 0) s_nf[gr * TB + b] = make_float2(inv_pow2(f), -0x1p-21f * sum);
     }
     __syncthreads();
 
@@ -292,31 +304,10 @@ __global__ void __launch_bounds__(kThreads, 1) linear4_kernel(const LinearArgs a
     uint32_t xcol[NT];
 #pragma unroll
     for (int n = 0; n < NT; ++n) xcol[n] = smem_u32(s_x) + min(8 * n + g, cols - 1) * xs + 16 * t;
-    // start values: -8 sum_k x, by the same product with the code 8 everywhere
-    for (int gr = warp; gr < nG; gr += kWarps)
-#pragma unroll
-      for (int n = 0; n < NT; ++n) {
-        float d[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const uint4 xv = lds128(xcol[n] + gr * 256 + i * 64);
-          mma_f16(d, 0x00080008u, 0x00080008u, 0x00800080u, 0x00800080u, xv.x, xv.y);
-          mma_f16(d, 0x00080008u, 0x00080008u, 0x00800080u, 0x00800080u, xv.z, xv.w);
-        }
-        if (g == 0) {
-          float2* nf = s_nf + gr * TB;
-          if (PARTS == 2) {
-            nf[4 * n + t].y = -(d[0] + d[1]);
-          } else {
-            nf[8 * n + 2 * t].y = -d[0];
-            nf[8 * n + 2 * t + 1].y = -d[1];
-          }
-        }
-      }
-    __syncthreads();
     const uint32_t nf0 = smem_u32(s_nf + NC * t);
 
     uint32_t slot = ring;
+    bool has_head = false, has_tail = false;
     for (int u = beg; u < end;) {
       const int n_units = min(nG - gr0, end - u);  // of this strip
 #pragma unroll
@@ -355,11 +346,14 @@ __global__ void __launch_bounds__(kThreads, 1) linear4_kernel(const LinearArgs a
         load(slot + after(scw.y));
         slot = slot == ring + (PF - 1) * kSlotBytes ? ring : slot + kSlotBytes;
         float d[2][NT][4];
+        uint4 xq[4][NT];
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+          for (int n = 0; n < NT; ++n) xq[i][n] = lds128(xa[n] + i * 64);
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          uint4 xv[NT];
-#pragma unroll
-          for (int n = 0; n < NT; ++n) xv[n] = lds128(xa[n] + i * 64);
+          const uint4(&xv)[NT] = xq[i];
 #pragma unroll
           for (int m = 0; m < 2; ++m) {
             const uint4 w4 = w[m][i >> 1];
@@ -401,41 +395,51 @@ __global__ void __launch_bounds__(kThreads, 1) linear4_kernel(const LinearArgs a
       // the strip's results, or this warp's part of them
       if (n_units == nG) {
         if (!use_res)
-          each([&](int row, int b, float v) { put(strip, row, b, v); });
+          each(acc, [&](int row, int b, float v) { put(strip, row, b, v); });
         else
-          each([&](int row, int b, float v) {
-            float* r = s_res + ((strip - s0) * kStrip + row) * a.B + b;
+          each(acc, [&](int row, int b, float v) {
+            float* r = s_res + ((strip - s0) * a.B + b) * kPartRow + row;
             *r = ph == 0 ? v : *r + v;
           });
+      } else if (gr0 > 0) {
+        has_head = true;
+#pragma unroll
+        for (int m = 0; m < 2; ++m)
+#pragma unroll
+          for (int n = 0; n < NT; ++n)
+#pragma unroll
+            for (int r = 0; r < 2; ++r)
+#pragma unroll
+              for (int e = 0; e < NC; ++e) head_acc[m][n][r][e] = acc[m][n][r][e];
       } else {
-        float* part = s_head + warp * kStrip * a.B;
-        if (gr0 == 0) {  // the range ends here: the ring has been read
-          cp_async_wait<0>();
-          __syncwarp();
-          part = tail(warp);
-        }
-        each([&](int row, int b, float v) { part[row * a.B + b] = v; });
+        has_tail = true;  // the range ends here
       }
       u += n_units;
       gr0 = 0;
       ++strip;
     }
+    cp_async_wait<0>();
+    __syncwarp();
+    if (has_head) each(head_acc, [&, p = head(warp)](int row, int b, float v) { p[b * kPartRow + row] = v; });
+    if (has_tail) each(acc, [&, p = tail(warp)](int row, int b, float v) { p[b * kPartRow + row] = v; });
     __syncthreads();
-    // strips that several warps share, in warp order
-    for (int s = s0 + warp; s < s1 && nG > 0; s += kWarps) {
-      const int from = (s - s0) * nG;
-      const int wa = range_of(U, from, W), wb = range_of(U, from + nG - 1, W);
-      if (wa == wb) continue;
-      for (int e = lane; e < kStrip * a.B; e += 32) {
-        // e runs over the rows of one token first: neighbours in the output
-        const int b = e / kStrip, row = e % kStrip;
-        float v = tail(wa)[row * a.B + b];
-        for (int w = wa + 1; w <= wb; ++w) v += s_head[(w * kStrip + row) * a.B + b];
+    // strips that several warps share, in warp order: the strip at the start of
+    // warp w's range, where w is the second to have a part of it; neighbouring
+    // threads take neighbouring channels of one token
+    for (int w0 = 0; w0 < W - 1; ++w0) {  // w = w0 + 1
+      const int s = s_cut[w0].x, wb = s_cut[w0].y;
+      if (s < 0) continue;
+      for (int e = threadIdx.x; e < kStrip * a.B; e += kThreads) {
+        const int row = e % kStrip, b = e / kStrip;
+        float v = tail(w0)[b * kPartRow + row];
+        const float* h = head(w0 + 1) + b * kPartRow + row;
+#pragma unroll 4
+        for (int w = w0 + 1; w <= wb; ++w, h += PF * kSlotBytes / 4) v += *h;
         if (use_res) {
-          float* r = s_res + ((s - s0) * kStrip + row) * a.B + b;
+          float* r = s_res + (s * a.B + b) * kPartRow + row;
           *r = ph == 0 ? v : *r + v;
         } else {
-          put(s, row, b, v);
+          put(s0 + s, row, b, v);
         }
       }
     }
@@ -448,12 +452,15 @@ __global__ void __launch_bounds__(kThreads, 1) linear4_kernel(const LinearArgs a
   // the cluster's CTAs share out the results; ranks are added in order (a rank
   // without groups holds none)
   const int ranks = min(a.cluster, (a.G + a.per_rank - 1) / a.per_rank);
-  const int E = (s1 - s0) * kStrip * a.B;
-  for (int e = rank * kThreads + threadIdx.x; e < E; e += a.cluster * kThreads) {
-    const int row = e % kStrip, b = e / kStrip % a.B, s = e / (kStrip * a.B);
-    const float* p = s_res + (s * kStrip + row) * a.B + b;
-    float v = a.cluster > 1 ? ld_peer(p, 0) : *p;
-    for (int r = 1; r < ranks; ++r) v += ld_peer(p, r);
+  for (int e = rank * kThreads + threadIdx.x; e < (s1 - s0) * kStrip * a.B; e += a.cluster * kThreads) {
+    const int row = e % kStrip, q = e / kStrip, s = q / a.B, b = q - s * a.B;
+    const float* p = s_res + q * kPartRow + row;
+    float part[8];
+#pragma unroll
+    for (int r = 0; r < 8; ++r) part[r] = r >= ranks ? 0.f : a.cluster > 1 ? ld_peer(p, r) : *p;
+    float v = part[0];
+#pragma unroll
+    for (int r = 1; r < 8; ++r) v += part[r];
     put(s0 + s, row, b, v);
   }
   if (a.cluster > 1) cluster_sync_all();  // no CTA leaves while its results are read
@@ -502,8 +509,9 @@ int col_tiles(int B, int dtype) {
   return cols <= 8 ? 1 : cols <= 16 ? 2 : 4;
 }
 
-// Units in flight per warp: 8 cover a small matrix's whole share at once; 4 or
-// 2 where x takes the room.
+// Units in flight per warp: 4 cover a small matrix's whole share at once; 3 or
+// 2 where x takes the room.  (With one, 16 tokens x 5120 ran at HBM's latency:
+// 83 us for 131072 channels.)
 template <int PF>
 Kernel pick_depth(int dtype, int nt) {
   switch (dtype) {
@@ -515,7 +523,7 @@ Kernel pick_depth(int dtype, int nt) {
   }
 }
 Kernel pick(int dtype, int nt, int depth) {
-  return depth == 8 ? pick_depth<8>(dtype, nt) : depth == 4 ? pick_depth<4>(dtype, nt) : pick_depth<2>(dtype, nt);
+  return depth == 4 ? pick_depth<4>(dtype, nt) : depth == 3 ? pick_depth<3>(dtype, nt) : pick_depth<2>(dtype, nt);
 }
 
 struct Plan {
@@ -523,12 +531,18 @@ struct Plan {
   size_t ring_at, smem;
 };
 
-size_t ring_bytes(int depth) { return (size_t)kWarps * depth * kSlotBytes; }
+size_t ring_bytes(int nt, int depth) { return (size_t)warps_of(nt) * depth * kSlotBytes; }
 
 // The cluster size whose busiest CTA has the least to do: its units (2 KB of
-// codes each, about 90 SM cycles at the copy bandwidth), plus what joining
-// across the cluster costs (about 1 us, 20 units), plus 30 per extra phase of
-// x (the rings run dry and x is converted again).
+// codes each, about 90 SM cycles at the copy bandwidth), plus what converting x
+// costs (15 cycles per column and group), plus what a launch in clusters and
+// the join across them costs, plus 30 per extra phase of x (the rings run dry).
+// Measured at 4096 x 4096, clusters of 1 / 2 / 4 / 8: one token 5.1 / 6.4 / 6.8
+// / 8.2 us, 16 tokens 9.2 / 9.3 / 9.4 / 10.8; at 8192 x 1024 6.0 / 5.5 / 5.8 /
+// 6.5 and 17.9 / 9.8 / 8.0 / 8.1; at 28672 x 8192 with 16 tokens 96 / 64 / 48 /
+// 43.
+constexpr double kJoin[4] = {0, 35, 45, 75};
+
 bool plan_linear4(const prox_linear4* L, int B, int dtype, Plan* best) {
   const int nt = col_tiles(B, dtype), parts = dtype == PROX_F32 ? 2 : 1;
   const int cols = B * parts, tb = 8 * nt / parts;
@@ -546,15 +560,15 @@ bool plan_linear4(const prox_linear4* L, int B, int dtype, Plan* best) {
     auto front = [&] {  // everything before the rings
       const int res = c > 1 || p.per_phase < p.per_rank ? p.per_clus : 0;
       return ((size_t)cols * (p.per_phase * 256 + kXPad) + (size_t)p.per_phase * tb * 8 +
-              (size_t)(kWarps + res) * kStrip * B * 4 + 15) & ~(size_t)15;
+              (size_t)res * kPartRow * B * 4 + 15) & ~(size_t)15;
     };
-    while (front() + ring_bytes(2) > kSmemLimit && p.per_phase > 1) p.per_phase = (p.per_phase + 1) / 2;
+    while (front() + ring_bytes(nt, 2) > kSmemLimit && p.per_phase > 1) p.per_phase = (p.per_phase + 1) / 2;
     p.ring_at = front();
-    if (p.ring_at + ring_bytes(2) > kSmemLimit) continue;
-    p.depth = p.ring_at + ring_bytes(8) <= kSmemLimit ? 8 : p.ring_at + ring_bytes(4) <= kSmemLimit ? 4 : 2;
-    p.smem = p.ring_at + ring_bytes(p.depth);
+    if (p.ring_at + ring_bytes(nt, 2) > kSmemLimit) continue;
+    for (p.depth = 4; p.ring_at + ring_bytes(nt, p.depth) > kSmemLimit;) --p.depth;
+    p.smem = p.ring_at + ring_bytes(nt, p.depth);
     const int phases = (p.per_rank + p.per_phase - 1) / p.per_phase;
-    const double cost = (double)p.per_clus * p.per_rank + (c > 1 ? 20.0 : 0.0) + 30.0 * (phases - 1);
+    const double cost = (double)p.per_clus * p.per_rank + 0.17 * cols * p.per_rank + kJoin[ci] + 30.0 * (phases - 1);
     if (cost < least) {
       least = cost;
       *best = p;
@@ -576,7 +590,7 @@ cudaError_t setup_linear4(prox_linear4* L) {
   for (int dtype : {PROX_F32, PROX_F16, PROX_BF16})
     for (int nt : {1, 2, 4}) {
       if (nt == 4 && dtype != PROX_F32) continue;
-      for (int depth : {2, 4, 8}) {
+      for (int depth : {2, 3, 4}) {
         cudaError_t e = cudaFuncSetAttribute(pick(dtype, nt, depth), cudaFuncAttributeMaxDynamicSharedMemorySize,
                                              kSmemLimit);
         if (e != cudaSuccess) return e;
@@ -586,7 +600,7 @@ cudaError_t setup_linear4(prox_linear4* L) {
   for (int ci = 1; ci < 4; ++ci) {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)(L->num_sms >> ci << ci), 1, 1);
-    cfg.blockDim = dim3(kThreads, 1, 1);
+    cfg.blockDim = dim3(warps_of(1) * 32, 1, 1);
     cfg.dynamicSmemBytes = kSmemLimit;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeClusterDimension;
@@ -627,7 +641,7 @@ cudaError_t launch_linear4(const prox_linear4* L, const void* x, int64_t x_strid
   a.x_vec = (reinterpret_cast<uintptr_t>(x) & 15) == 0 && (B == 1 || x_stride % (dtype == PROX_F32 ? 4 : 8) == 0);
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)(p.clusters * p.cluster), 1, 1);
-  cfg.blockDim = dim3(kThreads, 1, 1);
+  cfg.blockDim = dim3(warps_of(nt) * 32, 1, 1);
   cfg.dynamicSmemBytes = p.smem;
   cfg.stream = s;
   cudaLaunchAttribute attr[2];
