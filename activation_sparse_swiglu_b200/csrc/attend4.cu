@@ -3,24 +3,34 @@
 // Mathematics.  With K_j = ks_j q^K_j and V_j = vs_j q^V_j (integers q, one
 // fp16 scale per token and head) a query row needs
 //   t_j = (scale log2 e) ks_j (Q . q^K_j),   o = sum_j 2^(t_j - m) vs_j q^V_j / sum_j 2^(t_j - m),
-// so the scales multiply scores and probabilities, never the codes: both
-// products run on integers widened to fp16, exactly.
+// so the scales multiply scores and probabilities, never the codes.
 //
 // One warp keeps the running maximum, sum and output of the rows (query heads
-// of one group x new tokens) it works on, and takes 32 cache rows a step:
+// of one group x new tokens) it works on, and takes up to 64 cache rows a step:
 //   S^T = K Q^T   tokens are the M dimension, the rows the N = 8 columns, so a
 //                 group of up to 8 heads wastes no tensor work and a code is
-//                 widened once for all of them;
+//                 decoded once for all of them;
 //   O^T = V^T P^T the same, with P^T turned into the B operand by movmatrix.
 // K words are A fragments as they lie (the order of d inside a product is
 // free, so Q takes the codes' order); V needs pairs of tokens in one register,
 // one byte permute per word.  Which token stands in which fragment row is free
 // too, and chosen so that the shared-memory reads of K and V meet no bank
-// conflict at head_dim 128 (see token_of).
-// fp16 and bf16 queries are exact in fp16 (bf16 scaled by a power of two);
-// fp32 queries and their probabilities are split into hi + lo columns.
+// conflict at head_dim 128 and 256 (see token_of).
+//
+// The kernel is bound by issue before it is by HBM unless decoding is cheap.
+// fp16 and bf16 queries: a nibble masked out of a word is an fp16 subnormal
+// (spread8), 5/8 of an instruction per code; the offset 8 is taken off in the
+// sums' start values: -8 sum_d Q_d for a score, and -8 sum_j p_j for an output,
+// which one product with a constant gives in the right registers.  The
+// cancellation costs a few fp32 roundings of 8 sum p, invisible in a 16-bit
+// result.  fp32 queries are held to fp32: their codes are widened to exact
+// integers (9/8 instructions), queries and probabilities split into hi + lo
+// columns.  bf16 and fp32 queries are scaled by a power of two.  (Exact
+// widening for all types, 32 rows a step and a page lookup per 16-byte copy
+// took 1080 instructions per 32 rows and 132 us for 64 requests of the
+// 8B-shaped model, 0.35 of the copy bandwidth.)
 // Probabilities times vs are scaled by a power of two per step so that they
-// use fp16's range; each step's product starts from zero and joins the fp32
+// use fp16's range; each step's product starts afresh and joins the fp32
 // output with one fused multiply-add, so the tensor core's own sums stay short.
 //
 // Split.  The unit is 32 rows of one (request, kv head).  All units of the
@@ -42,10 +52,15 @@ namespace {
 
 using namespace q4;
 
-constexpr int kStep = 32;    // cache rows of one step
+constexpr int kUnit = 32;    // cache rows that are dealt out together
 constexpr int kMaxWarps = 12;
-constexpr int kStages = 3;   // steps in flight or in use per warp
 constexpr int kSmemLimit = 227 * 1024;
+
+// Cache rows of a step, and steps in flight or in use per warp.
+constexpr int step_rows(int D) { return D == 256 ? 32 : 64; }
+// Warps: as many as the registers of the column tiles allow.
+constexpr int warps_of(int D, int nt) { return D == 256 || nt == 2 ? 8 : kMaxWarps; }
+constexpr int stages_of(int D, int nt) { return warps_of(D, nt) == 8 ? 3 : 2; }
 
 struct AttendArgs {
   Attend4Call c;
@@ -56,7 +71,8 @@ struct AttendArgs {
   int pages, heads, page_shift;
   int G, R, blocks;  // heads per kv head, rows per kv head, row blocks
   int* err;
-  float* part;
+  float* part;       // [2 * CTAs] parts that go on in another CTA
+  float* warp_part;  // [CTAs * warps] parts that end amid a warp's range
   int* arrived;
   bool q_vec;
 };
@@ -80,9 +96,10 @@ __device__ __forceinline__ int v_piece(int row, int j) {
   return row * (D / 2) + 16 * j;
 }
 
+// A stage: K rows, V rows, their scales, and those scales as the step uses them.
 template <int D>
 constexpr int stage_bytes() {
-  return kStep * D + kStep * 4;
+  return step_rows(D) * (D + 4);
 }
 // One partial result: [rows][D] output, then maxima and sums.
 constexpr int part_floats(int rows, int D) { return rows * D + 2 * rows; }
@@ -93,34 +110,40 @@ __device__ __forceinline__ uint32_t prmt(uint32_t a, uint32_t b, uint32_t sel) {
   return r;
 }
 
-// A position in the sequence of units: chunk c of n of (request b, head block hb).
+// A position in the sequence of units: unit c of n of (request b, head block hb).
 struct Cursor {
   int b, hb, c, n, len;
-  long long beg;  // unit of chunk 0
+  long long beg;  // number of unit 0
 };
 
 template <int DT, int D, int NT>
-__global__ void __launch_bounds__(kMaxWarps * 32, 1) attend4_kernel(const AttendArgs a) {
+__global__ void __launch_bounds__(warps_of(D, NT) * 32, 1) attend4_kernel(const AttendArgs a) {
   using T = typename Act<DT>::T;
   constexpr int PARTS = DT == PROX_F32 ? 2 : 1;
+  constexpr bool EXACT = PARTS == 2;   // codes as exact integers, not offset subnormals
   constexpr int RB = 8 * NT / PARTS;   // rows of a block
   constexpr int NC = 2 / PARTS;        // rows a thread has per column tile
   constexpr int KW = D / 32;           // K words per thread and token
   constexpr int VW = D / 64;           // V words per thread and token
   constexpr int PIECES = D / 32;       // 16-byte pieces of a row
+  constexpr int ROWS = step_rows(D);
+  constexpr int MT = ROWS / 16;        // tiles of 16 tokens
+  constexpr int STAGES = stages_of(D, NT);
   constexpr int SB = stage_bytes<D>();
   constexpr int SLOT = part_floats(RB, D);
+  static_assert(SLOT * 4 <= STAGES * SB, "a part fits a ring");
   const Attend4Call& c = a.c;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
   const int g = lane >> 2, t = lane & 3;
 
   extern __shared__ __align__(16) char smem[];
-  char* ring = smem + (size_t)warp * kStages * SB;
-  float* heads_part = reinterpret_cast<float*>(smem + (size_t)warps * kStages * SB);  // [warps][SLOT]
-  int* pre = reinterpret_cast<int*>(heads_part + (size_t)warps * SLOT);               // [B + 1]
+  const uint32_t ring = smem_u32(smem) + warp * (STAGES * SB);
+  // the step's scales, ready for use: (ks scale log2 e, vs times its power of two)
+  const uint32_t sc_at = smem_u32(smem) + warps * (STAGES * SB) + warp * (ROWS * 8);
+  int* pre = reinterpret_cast<int*>(smem + (size_t)warps * (STAGES * SB + ROWS * 8));  // [B + 1]
   __shared__ long long s_scan[33];
   __shared__ long long s_head_seg[kMaxWarps], s_tail_seg[kMaxWarps];  // first unit of the context, -1: none
-  __shared__ int s_head_done[kMaxWarps];
+  __shared__ int s_head_done[kMaxWarps];  // 0: goes on; 1: ends with the range; 2: before it
   __shared__ int s_last;
 
   pdl_wait();
@@ -134,13 +157,13 @@ __global__ void __launch_bounds__(kMaxWarps * 32, 1) attend4_kernel(const Attend
   for (int i = rlo; i < rhi; ++i) {
     const int len = c.lens[i];
     if ((len < 0 || len > max_len) && blockIdx.x == 0) atomicOr(a.err, PROX_DEVERR_LEN);
-    mine += max(1, (min(max(len, 0), max_len) + kStep - 1) / kStep);
+    mine += max(1, (min(max(len, 0), max_len) + kUnit - 1) / kUnit);
   }
   long long total;
   long long at = block_exclusive_scan(mine, s_scan, &total);
   for (int i = rlo; i < rhi; ++i) {
     pre[i] = (int)at;
-    at += max(1, (min(max(c.lens[i], 0), max_len) + kStep - 1) / kStep);
+    at += max(1, (min(max(c.lens[i], 0), max_len) + kUnit - 1) / kUnit);
   }
   if (threadIdx.x == 0) pre[c.B] = (int)total;
   if (threadIdx.x < kMaxWarps) s_head_seg[threadIdx.x] = s_tail_seg[threadIdx.x] = -1;
@@ -177,8 +200,9 @@ __global__ void __launch_bounds__(kMaxWarps * 32, 1) attend4_kernel(const Attend
     s.beg = u - s.c;
     return s;
   };
-  auto advance = [&](Cursor& s) {  // not past the last unit
-    if (++s.c < s.n) return;
+  // n units on, to the next context at its end (not past the last unit)
+  auto advance = [&](Cursor& s, int n) {
+    if ((s.c += n) < s.n) return;
     s.beg += s.n;
     s.c = 0;
     if (++s.hb == H) {
@@ -186,45 +210,48 @@ __global__ void __launch_bounds__(kMaxWarps * 32, 1) attend4_kernel(const Attend
       if (++s.b < c.B) enter(s);
     }
   };
+  // units of the step at s, with `left` to the range's end
+  auto units = [&](const Cursor& s, long long left) {
+    return (int)min((long long)min(s.n - s.c, ROWS / kUnit), left);
+  };
 
-  // ---- producer: the copies of one step, one page lookup ahead --------------
-  int pid[2] = {0, 0};
-  auto lookup = [&](const Cursor& s) {
+  // ---- producer: the copies of one step, the page lookups one step ahead ------
+  constexpr int RPI = 32 / PIECES;  // rows of one copy instruction of the warp
+  int pid[MT];
+  auto lookup = [&](const Cursor& s, int n) {
     const int32_t* row = c.table + s.b * c.table_stride;
+    const int end = min(s.len, (s.c + n) * kUnit);
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      const int tok = s.c * kStep + 16 * h;
-      int id = 0;
-      if (tok < s.len) {
-        id = row[tok >> a.page_shift];
-        if (id < 0 || id >= a.pages) {
-          atomicOr(a.err, PROX_DEVERR_PAGE);
-          id = 0;
-        }
-      }
-      pid[h] = id;
+    for (int h = 0; h < MT; ++h) {
+      const int tok = s.c * kUnit + 16 * h;
+      pid[h] = tok < end ? row[tok >> a.page_shift] : -1;
     }
   };
   const int page_mask = (1 << a.page_shift) - 1;
-  auto copy = [&](const Cursor& s, int stage) {
-    char* dst = ring + stage * SB;
-    const int tok0 = s.c * kStep, head = s.hb / a.blocks;
+  const int src_at = lane / PIECES * (D / 2) + lane % PIECES * 16;
+  const int k_at = k_piece<D>(lane / PIECES, lane % PIECES), v_at = v_piece<D>(lane / PIECES, lane % PIECES);
+  auto copy = [&](const Cursor& s, int n, uint32_t dst) {
+    const int end = min(s.len, (s.c + n) * kUnit), head = s.hb / a.blocks;
 #pragma unroll
-    for (int i = 0; i < PIECES; ++i) {
-      const int id = i * 32 + lane, row = id / PIECES, j = id % PIECES;
-      if (tok0 + row < s.len) {
-        const int64_t r = ((int64_t)((row < 16 ? pid[0] : pid[1])) * a.heads + head << a.page_shift) +
-                          ((tok0 + row) & page_mask);
-        cp_async16(smem_u32(dst) + k_piece<D>(row, j), a.k + r * (D / 2) + 16 * j);
-        cp_async16(smem_u32(dst) + kStep * D / 2 + v_piece<D>(row, j), a.v + r * (D / 2) + 16 * j);
+    for (int h = 0; h < MT; ++h) {  // 16 rows lie in one page
+      const int tok = s.c * kUnit + 16 * h;
+      if (tok >= end) break;
+      int id = pid[h];
+      if ((unsigned)id >= (unsigned)a.pages) {
+        atomicOr(a.err, PROX_DEVERR_PAGE);
+        id = 0;
       }
-    }
-    if (lane < 8) {  // scales: four pieces of 8 tokens each
-      const int q = lane & 3;
-      if (tok0 + 8 * q < s.len) {
-        const int64_t r = ((int64_t)(pid[q >> 1]) * a.heads + head << a.page_shift) + ((tok0 + 8 * q) & page_mask);
-        cp_async16(smem_u32(dst) + kStep * D + (lane >> 2) * kStep * 2 + 16 * q, (lane < 4 ? a.ks : a.vs) + r);
+      const int64_t r = ((int64_t)id * a.heads + head << a.page_shift) + (tok & page_mask);
+      const uint8_t* kp = a.k + r * (D / 2) + src_at;
+      const uint8_t* vp = a.v + r * (D / 2) + src_at;
+#pragma unroll
+      for (int i = 0; i < 16 / RPI; ++i) {
+        cp_async16(dst + k_at + (16 * h + RPI * i) * (D / 2), kp + RPI * i * (D / 2));
+        cp_async16(dst + v_at + (ROWS + 16 * h + RPI * i) * (D / 2), vp + RPI * i * (D / 2));
       }
+      if (lane < 4)  // two pieces of eight scales each
+        cp_async16(dst + ROWS * D + (lane >> 1) * (ROWS * 2) + 32 * h + 16 * (lane & 1),
+                   (lane < 2 ? a.ks : a.vs) + r + 8 * (lane & 1));
     }
   };
 
@@ -233,7 +260,9 @@ __global__ void __launch_bounds__(kMaxWarps * 32, 1) attend4_kernel(const Attend
   float O[VW][4][2][NT][NC];   // [word][tile][row half][column tile][column]
   float mx[NT][NC], sum[NT][NC];
   int lim[NT][NC];             // last visible token
-  float cm = 0.f;              // scale log2(e) / the queries' power of two
+  float cm = 0.f;              // scale log2(e) / the queries' power of two (and 2^24)
+  float s0[NT][2];             // a score's start value per column
+  float vscale = 1.f;          // O's power of two
 
   auto row_of = [&](int nt, int e) { return PARTS == 2 ? 4 * nt + t : 8 * nt + 2 * t + e; };
   auto out_at = [&](const Cursor& s, int row) {  // element (b, i, h, 0) of row `row` of s's block, -1: none
@@ -269,24 +298,37 @@ __global__ void __launch_bounds__(kMaxWarps * 32, 1) attend4_kernel(const Attend
       f = normaliser(top);
     }
     cm = c.scale * 1.4426950408889634f * inv_pow2(f);
+    if (!EXACT) cm *= 0x1p24f;
+    vscale = 1.f;
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
+      float total = 0.f;  // of the column's Q as the products see it
 #pragma unroll
       for (int i = 0; i < KW; ++i) {
         uint32_t w[8];
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
-          const float y = qv[nt][8 * i + j] * f;
+          // odd nibbles stand 4 bits higher in the subnormals
+          const float y = qv[nt][8 * i + j] * (!EXACT && (j & 1) ? 0.0625f * f : f);
           const __half hi = __float2half_rn(y);
           __half v = hi;
           if (PARTS == 2 && (g & 1)) v = __float2half_rn(y - __half2float(hi));
           w[j] = __half_as_ushort(v);
+          total = fmaf(__half2float(v), j & 1 ? 16.f : 1.f, total);
         }
 #pragma unroll
         for (int h = 0; h < 2; ++h) {  // pairs (2h, 2h + 4) and (2h + 1, 2h + 5)
           qf[i][h][nt][0] = w[2 * h] | w[2 * h + 4] << 16;
           qf[i][h][nt][1] = w[2 * h + 1] | w[2 * h + 5] << 16;
         }
+      }
+      if (EXACT) {
+        s0[nt][0] = s0[nt][1] = 0.f;
+      } else {
+        total += __shfl_xor_sync(0xffffffffu, total, 1);
+        total += __shfl_xor_sync(0xffffffffu, total, 2);
+        s0[nt][0] = -0x1p-21f * __shfl_sync(0xffffffffu, total, 8 * t);
+        s0[nt][1] = -0x1p-21f * __shfl_sync(0xffffffffu, total, 8 * t + 4);
       }
 #pragma unroll
       for (int e = 0; e < NC; ++e) {
@@ -308,101 +350,138 @@ __global__ void __launch_bounds__(kMaxWarps * 32, 1) attend4_kernel(const Attend
             for (int e = 0; e < NC; ++e) O[x][q][h][nt][e] = 0.f;
   };
 
-  auto step = [&](const Cursor& s, int stage) {
-    const char* st = ring + stage * SB;
-    const __half* s_ks = reinterpret_cast<const __half*>(st + kStep * D);
-    const __half* s_vs = s_ks + kStep;
-    const int tok0 = s.c * kStep;
-    // scores: token rows token_of(g) (+ 8), two tiles of 16 tokens
-    float S[2][NT][4];
-    float ksc[2][2], vsc[2][2];
-    float vtop = 0.f;
+  auto decode = [&](uint32_t w, uint32_t(&r)[4]) {
+    if (EXACT)
+      widen8(w, r);
+    else
+      spread8(w, r);
+  };
+  auto step = [&](const Cursor& s, int n, uint32_t st) {
+    const int tok0 = s.c * kUnit, end = min(s.len, tok0 + n * kUnit);
+    // the step's scales; rows behind the end may hold anything and count as 0
+    float ksv[ROWS / 32], vsv[ROWS / 32];
+    uint32_t vbits = 0;
+#pragma unroll
+    for (int i = 0; i < ROWS / 32; ++i) {
+      const int row = 32 * i + lane;
+      const uint32_t kb = lds16(st + ROWS * D + 2 * row), vb = lds16(st + ROWS * (D + 2) + 2 * row);
+      const bool there = tok0 + row < end;
+      ksv[i] = there ? __half2float(__ushort_as_half((unsigned short)kb)) * cm : 0.f;
+      vsv[i] = there ? __half2float(__ushort_as_half((unsigned short)vb)) : 0.f;
+      const uint32_t m = vb & 0x7FFFu;  // magnitudes order like their bits; infinity and NaN do not count
+      if (there && m < 0x7C00u) vbits = max(vbits, m);
+    }
+    vbits = __reduce_max_sync(0xffffffffu, vbits);
+    const float vf = normaliser(__half2float(__ushort_as_half((unsigned short)vbits)));
+#pragma unroll
+    for (int i = 0; i < ROWS / 32; ++i)
+      sts64(sc_at + (32 * i + lane) * 8, __float_as_uint(ksv[i]), __float_as_uint(vsv[i] * vf));
+
+    // scores: token rows token_of(g) (+ 8) of MT tiles of 16 tokens
+    float S[MT][NT][4];
     const int tr = token_of(g);
 #pragma unroll
-    for (int m = 0; m < 2; ++m) {
-#pragma unroll
-      for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) S[m][nt][i] = 0.f;
+    for (int m = 0; m < MT; ++m) {
       uint32_t w[2][KW];
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
-        const int row = 16 * m + 8 * h + tr;
+        const int row = 16 * m + 8 * h;  // + tr
         if constexpr (D == 64) {
-          const uint2 u = *reinterpret_cast<const uint2*>(st + row * 32 + 8 * t);
+          const uint2 u = lds64(st + (row + tr) * 32 + 8 * t);
           w[h][0] = u.x, w[h][1] = u.y;
         } else {
 #pragma unroll
           for (int p = 0; p < KW / 4; ++p) {
-            const uint4 u = lds_v4(st + k_piece<D>(row, t + 4 * p));
+            // (adding 16 m + 8 h rows leaves the pieces' order as it is)
+            const uint4 u = lds128(st + k_piece<D>(tr, t + 4 * p) + row * (D / 2));
             w[h][4 * p] = u.x, w[h][4 * p + 1] = u.y, w[h][4 * p + 2] = u.z, w[h][4 * p + 3] = u.w;
           }
         }
-        const bool there = tok0 + row < s.len;
-        ksc[m][h] = there ? __half2float(s_ks[row]) * cm : 0.f;
-        vsc[m][h] = there ? __half2float(s_vs[row]) : 0.f;
-        vtop = fmaxf(vtop, fabsf(vsc[m][h]) <= 65504.f ? fabsf(vsc[m][h]) : 0.f);
       }
 #pragma unroll
       for (int i = 0; i < KW; ++i) {
         uint32_t ra[4], rb[4];
-        widen8(w[0][i], ra);
-        widen8(w[1][i], rb);
+        decode(w[0][i], ra);
+        decode(w[1][i], rb);
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
-          mma_f16(S[m][nt], ra[0], rb[0], ra[1], rb[1], qf[i][0][nt][0], qf[i][0][nt][1]);
+          if (i == 0)
+            mma_f16(S[m][nt], ra[0], rb[0], ra[1], rb[1], qf[i][0][nt][0], qf[i][0][nt][1], s0[nt][0], s0[nt][1],
+                    s0[nt][0], s0[nt][1]);
+          else
+            mma_f16(S[m][nt], ra[0], rb[0], ra[1], rb[1], qf[i][0][nt][0], qf[i][0][nt][1]);
           mma_f16(S[m][nt], ra[2], rb[2], ra[3], rb[3], qf[i][1][nt][0], qf[i][1][nt][1]);
         }
       }
     }
+    __syncwarp();  // the scales are there
+    float ksc[MT][2], vsc[MT][2];
 #pragma unroll
-    for (int o = 4; o < 32; o <<= 1) vtop = fmaxf(vtop, __shfl_xor_sync(0xffffffffu, vtop, o));
-    const float vf = normaliser(vtop), vinv = inv_pow2(vf);
+    for (int m = 0; m < MT; ++m)
 #pragma unroll
-    for (int m = 0; m < 2; ++m)
-#pragma unroll
-      for (int h = 0; h < 2; ++h) vsc[m][h] *= vf;
+      for (int h = 0; h < 2; ++h) {
+        const uint2 u = lds64(sc_at + (16 * m + 8 * h + tr) * 8);
+        ksc[m][h] = __uint_as_float(u.x), vsc[m][h] = __uint_as_float(u.y);
+      }
 
     // running softmax, then P^T as B fragments
-    const bool masked = tok0 + kStep - 1 > s.len - c.Tq;
-    uint32_t pf[2][NT][2];
+    const bool masked = tok0 + ROWS > min(s.len - c.Tq + 1, end);
+    uint32_t pf[MT][NT][2];
     float alpha[NT][NC];
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
-      float p[2][2][NC];
+      float p[MT][2][NC];
 #pragma unroll
-      for (int m = 0; m < 2; ++m)
+      for (int m = 0; m < MT; ++m)
 #pragma unroll
         for (int h = 0; h < 2; ++h)
 #pragma unroll
           for (int e = 0; e < NC; ++e) {
             const float z = PARTS == 2 ? S[m][nt][2 * h] + S[m][nt][2 * h + 1] : S[m][nt][2 * h + e];
             p[m][h][e] = z * ksc[m][h];
-            if (masked && tok0 + 16 * m + 8 * h + tr > lim[nt][e]) p[m][h][e] = -INFINITY;
           }
+      if (masked) {
+#pragma unroll
+        for (int m = 0; m < MT; ++m)
+#pragma unroll
+          for (int h = 0; h < 2; ++h)
+#pragma unroll
+            for (int e = 0; e < NC; ++e)
+              if (tok0 + 16 * m + 8 * h + tr > min(lim[nt][e], end - 1)) p[m][h][e] = -INFINITY;
+      }
 #pragma unroll
       for (int e = 0; e < NC; ++e) {
-        float top = fmaxf(fmaxf(p[0][0][e], p[0][1][e]), fmaxf(p[1][0][e], p[1][1][e]));
+        float top = mx[nt][e];
+#pragma unroll
+        for (int m = 0; m < MT; ++m) top = fmaxf(top, fmaxf(p[m][0][e], p[m][1][e]));
 #pragma unroll
         for (int o = 4; o < 32; o <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-        top = fmaxf(top, mx[nt][e]);
         const float base = top == -INFINITY ? 0.f : top;
-        alpha[nt][e] = exp2_fast(mx[nt][e] - base);
+        const float al = exp2_fast(mx[nt][e] - base);
         mx[nt][e] = top;
         float add = 0.f;
 #pragma unroll
-        for (int m = 0; m < 2; ++m)
+        for (int m = 0; m < MT; ++m)
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
-            const float x = p[m][h][e];
-            const float y = exp2_fast(x - base);
+            const float y = exp2_fast(p[m][h][e] - base);
             add += y;
-            p[m][h][e] = masked && tok0 + 16 * m + 8 * h + tr > lim[nt][e] ? 0.f : y * vsc[m][h];
+            p[m][h][e] = y * vsc[m][h];
           }
-        sum[nt][e] = fmaf(sum[nt][e], alpha[nt][e], add);
+        sum[nt][e] = fmaf(sum[nt][e], al, add);
+        alpha[nt][e] = al * (vf * inv_pow2(vscale));
+      }
+      if (masked) {  // an infinite or NaN scale of a masked row times 0 is NaN
+#pragma unroll
+        for (int m = 0; m < MT; ++m)
+#pragma unroll
+          for (int h = 0; h < 2; ++h)
+#pragma unroll
+            for (int e = 0; e < NC; ++e)
+              if (tok0 + 16 * m + 8 * h + tr > min(lim[nt][e], end - 1)) p[m][h][e] = 0.f;
       }
 #pragma unroll
-      for (int m = 0; m < 2; ++m)
+      for (int m = 0; m < MT; ++m)
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
           __half2 v;
@@ -415,60 +494,80 @@ __global__ void __launch_bounds__(kMaxWarps * 32, 1) attend4_kernel(const Attend
           pf[m][nt][h] = transpose8(h2_bits(v));
         }
     }
+    vscale = vf;
 
-    // O^T += V^T P^T: thread g has VW words of 8 values of each token
-    const char* sv = st + kStep * D / 2;
-    uint32_t vw[2][4][VW];  // [16 tokens][tokens of slots 2t, 2t + 1, 2t + 8, 2t + 9]
+    // O^T += V^T P^T: thread g has VW words of 8 values of each token.  Start
+    // values: -8 sum_j p_j 2^-24, 16 times that in the rows of odd nibbles.
+    float o0[NT][4];
 #pragma unroll
-    for (int m = 0; m < 2; ++m)
+    for (int nt = 0; nt < NT; ++nt) {
+      if (EXACT) {
+        o0[nt][0] = o0[nt][1] = o0[nt][2] = o0[nt][3] = 0.f;
+      } else {
+        mma_f16(o0[nt], 0x80088008u, 0x80808080u, 0x80088008u, 0x80808080u, pf[0][nt][0], pf[0][nt][1], 0.f, 0.f, 0.f, 0.f);
 #pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        const int row = 16 * m + 8 * (q >> 1) + ((q & 1) ? 4 + (t ^ 1) : t);
-        if constexpr (D == 64) {
-          vw[m][q][0] = *reinterpret_cast<const uint32_t*>(sv + row * 32 + 4 * g);
-        } else if constexpr (D == 128) {
-          const uint2 u = *reinterpret_cast<const uint2*>(sv + v_piece<D>(row, g >> 1) + 8 * (g & 1));
-          vw[m][q][0] = u.x, vw[m][q][1] = u.y;
-        } else {
-          const uint4 u = lds_v4(sv + v_piece<D>(row, g));
-          vw[m][q][0] = u.x, vw[m][q][1] = u.y, vw[m][q][2] = u.z, vw[m][q][3] = u.w;
-        }
+        for (int m = 1; m < MT; ++m)
+          mma_f16(o0[nt], 0x80088008u, 0x80808080u, 0x80088008u, 0x80808080u, pf[m][nt][0], pf[m][nt][1]);
       }
+    }
+    const uint32_t sv = st + ROWS * (D / 2);
 #pragma unroll
-    for (int x = 0; x < VW; ++x)
+    for (int x0 = 0; x0 < VW; x0 += 2) {  // two words at a time (head_dim 64 has one)
+      constexpr int XN = VW < 2 ? 1 : 2;
+      float part[XN][4][NT][4];
 #pragma unroll
-      for (int half = 0; half < 2; ++half) {  // values 8x + 4 half .. + 3 of the thread
-        float part[2][NT][4];
+      for (int m = 0; m < MT; ++m) {
+        uint32_t vw[4][XN];  // tokens of slots 2t, 2t + 1, 2t + 8, 2t + 9
 #pragma unroll
-        for (int q = 0; q < 2; ++q)
-#pragma unroll
-          for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-            for (int i = 0; i < 4; ++i) part[q][nt][i] = 0.f;
-#pragma unroll
-        for (int m = 0; m < 2; ++m) {
-          uint32_t r0[4], r1[4];
-          widen8(prmt(vw[m][0][x], vw[m][1][x], half ? 0x7632 : 0x5410), r0);
-          widen8(prmt(vw[m][2][x], vw[m][3][x], half ? 0x7632 : 0x5410), r1);
-#pragma unroll
-          for (int nt = 0; nt < NT; ++nt) {
-            mma_f16(part[0][nt], r0[0], r0[1], r1[0], r1[1], pf[m][nt][0], pf[m][nt][1]);
-            mma_f16(part[1][nt], r0[2], r0[3], r1[2], r1[3], pf[m][nt][0], pf[m][nt][1]);
+        for (int q = 0; q < 4; ++q) {
+          const int in8 = (q & 1) ? 4 + (t ^ 1) : t, row = 16 * m + 8 * (q >> 1);  // row + in8
+          if constexpr (D == 64) {
+            vw[q][0] = lds32(sv + (row + in8) * 32 + 4 * g);
+          } else if constexpr (D == 128) {
+            const uint2 u = lds64(sv + v_piece<D>(in8, g >> 1) + row * (D / 2) + 8 * (g & 1));
+            vw[q][0] = u.x, vw[q][1] = u.y;
+          } else {
+            const uint2 u = lds64(sv + v_piece<D>(in8, g) + row * (D / 2) + 4 * x0);
+            vw[q][0] = u.x, vw[q][1] = u.y;
           }
         }
 #pragma unroll
-        for (int q = 0; q < 2; ++q)
+        for (int x = 0; x < XN; ++x)
+#pragma unroll
+          for (int half = 0; half < 2; ++half) {  // values 8x + 4 half .. + 3 of the thread
+            uint32_t r0[4], r1[4];
+            decode(prmt(vw[0][x], vw[1][x], half ? 0x7632 : 0x5410), r0);
+            decode(prmt(vw[2][x], vw[3][x], half ? 0x7632 : 0x5410), r1);
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) {
+              float(&d0)[4] = part[x][2 * half][nt];
+              float(&d1)[4] = part[x][2 * half + 1][nt];
+              const uint32_t b0 = pf[m][nt][0], b1 = pf[m][nt][1];
+              if (m == 0) {
+                mma_f16(d0, r0[0], r0[1], r1[0], r1[1], b0, b1, o0[nt][0], o0[nt][1], o0[nt][2], o0[nt][3]);
+                mma_f16(d1, r0[2], r0[3], r1[2], r1[3], b0, b1, o0[nt][0], o0[nt][1], o0[nt][2], o0[nt][3]);
+              } else {
+                mma_f16(d0, r0[0], r0[1], r1[0], r1[1], b0, b1);
+                mma_f16(d1, r0[2], r0[3], r1[2], r1[3], b0, b1);
+              }
+            }
+          }
+      }
+#pragma unroll
+      for (int x = 0; x < XN; ++x)
+#pragma unroll
+        for (int q = 0; q < 4; ++q)
 #pragma unroll
           for (int h = 0; h < 2; ++h)
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
               for (int e = 0; e < NC; ++e) {
-                const float z = PARTS == 2 ? part[q][nt][2 * h] + part[q][nt][2 * h + 1] : part[q][nt][2 * h + e];
-                float& o = O[x][2 * half + q][h][nt][e];
-                o = fmaf(o, alpha[nt][e], z * vinv);
+                const float(&d)[4] = part[x][q][nt];
+                float& o = O[x0 + x][q][h][nt][e];
+                o = fmaf(o, alpha[nt][e], PARTS == 2 ? d[2 * h] + d[2 * h + 1] : d[2 * h + e]);
               }
-      }
+    }
   };
 
   // The thread's 8 VW contiguous values of a row, times f.
@@ -478,9 +577,10 @@ __global__ void __launch_bounds__(kMaxWarps * 32, 1) attend4_kernel(const Attend
 #pragma unroll
       for (int q = 0; q < 4; ++q)
 #pragma unroll
-        for (int h = 0; h < 2; ++h) y[8 * x + 2 * q + h] = O[x][q][h][nt][e] * f;
+        for (int h = 0; h < 2; ++h) y[8 * x + 2 * q + h] = O[x][q][h][nt][e] * (!EXACT && h ? 0.0625f * f : f);
   };
   auto end_rows = [&](const Cursor& s, float* slot) {
+    const float unscale = (EXACT ? 1.f : 0x1p24f) * inv_pow2(vscale);
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -491,77 +591,86 @@ __global__ void __launch_bounds__(kMaxWarps * 32, 1) attend4_kernel(const Attend
         const int row = row_of(nt, e);
         float y[8 * VW];
         if (slot) {
-          values(nt, e, 1.f, y);
+          values(nt, e, unscale, y);
           store_vals<PROX_F32, 8 * VW>(slot + row * D + 8 * VW * g, true, y);
           if (g == 0) slot[RB * D + row] = mx[nt][e], slot[RB * D + RB + row] = l;
           continue;
         }
         const int64_t o = out_at(s, row);
         if (o < 0) continue;
-        values(nt, e, l == 0.f ? 0.f : 1.f / l, y);
+        values(nt, e, l == 0.f ? 0.f : unscale / l, y);
         store_vals<DT, 8 * VW>(static_cast<T*>(c.out) + o + 8 * VW * g, true, y);
         if (c.lse && g == 0) c.lse[o / D] = l == 0.f ? -INFINITY : 0.6931471805599453f * (mx[nt][e] + log2f(l));
       }
   };
 
   // ---- the warp's range -------------------------------------------------------
+  float* warp_part = a.warp_part + (size_t)(blockIdx.x * warps + warp) * SLOT;
   if (wb < we) {
     Cursor cur = seek(wb), pro = cur;
-    long long pu = wb;  // next unit to copy
-    lookup(pro);
-    auto issue = [&](int stage) {
-      if (pu < we) {
-        copy(pro, stage);
-        if (++pu < we) {
-          advance(pro);
-          lookup(pro);
+    long long left = we - wb, pleft = left;  // units to compute, to copy
+    int pn = units(pro, pleft);
+    lookup(pro, pn);
+    auto issue = [&](uint32_t dst) {
+      if (pleft > 0) {
+        copy(pro, pn, dst);
+        if ((pleft -= pn) > 0) {
+          advance(pro, pn);
+          pn = units(pro, pleft);
+          lookup(pro, pn);
         }
       }
       cp_async_commit();
     };
 #pragma unroll
-    for (int i = 0; i < kStages - 1; ++i) issue(i);
-    int stage = 0;
+    for (int i = 0; i < STAGES - 1; ++i) issue(ring + i * SB);
+    uint32_t st = ring, next = ring + (STAGES - 1) * SB;  // the stage to read, to fill
     begin_rows(cur);
-    for (long long u = wb; u < we; ++u) {
-      cp_async_wait<kStages - 2>();
+    while (left > 0) {
+      const int n = units(cur, left);
+      cp_async_wait<STAGES - 2>();
       __syncwarp();
-      issue(stage == 0 ? kStages - 1 : stage - 1);
-      step(cur, stage);
-      stage = stage + 1 == kStages ? 0 : stage + 1;
-      const bool ends = cur.c + 1 == cur.n;
-      if (ends || u + 1 == we) {
+      issue(next);
+      next = st;
+      step(cur, n, st);
+      st = st == ring + (STAGES - 1) * SB ? ring : st + SB;
+      left -= n;
+      const bool ends = cur.c + n == cur.n;
+      if (ends || left == 0) {
         float* slot = nullptr;
-        if (cur.beg < wb) {
-          slot = heads_part + (size_t)warp * SLOT;
-          if (lane == 0) s_head_seg[warp] = cur.beg, s_head_done[warp] = ends;
-        } else if (!ends) {
-          // the warp's copies are done and read: its ring holds the part
-          cp_async_wait<0>();
-          __syncwarp();
-          slot = reinterpret_cast<float*>(ring);
-          if (lane == 0) s_tail_seg[warp] = cur.beg;
+        if (cur.beg < wb || !ends) {  // a part; at the range's end the ring is free for it
+          slot = left > 0 ? warp_part : reinterpret_cast<float*>(smem + (size_t)warp * (STAGES * SB));
+          if (left == 0) {
+            cp_async_wait<0>();
+            __syncwarp();
+          }
+          if (lane == 0) {
+            if (cur.beg < wb)
+              s_head_seg[warp] = cur.beg, s_head_done[warp] = !ends ? 0 : left > 0 ? 2 : 1;
+            else
+              s_tail_seg[warp] = cur.beg;
+          }
         }
         end_rows(cur, slot);
-        if (u + 1 < we) {
-          advance(cur);
+        if (left > 0) {
+          advance(cur, n);
           begin_rows(cur);
         }
       } else {
-        advance(cur);
+        advance(cur, n);
       }
     }
   }
   __syncthreads();
 
   // ---- contexts that several warps or CTAs share -------------------------------
-  // `n` parts of one context, the i-th at part(i) (in shared memory, or written
-  // by other CTAs): joined in order into the output, or into one part at `to`.
-  auto join = [&](auto shared, int n, auto&& part, const Cursor& s, float* to) {
-    constexpr bool kShared = decltype(shared)::value;
-    auto ld1 = [](const float* p) { return kShared ? *p : __ldcg(p); };
+  // `n` parts of one context, the i-th at part(i) (this CTA's own, or written by
+  // other CTAs): joined in order into the output, or into one part at `to`.
+  auto join = [&](auto own, int n, auto&& part, const Cursor& s, float* to) {
+    constexpr bool kOwn = decltype(own)::value;
+    auto ld1 = [](const float* p) { return kOwn ? *p : __ldcg(p); };
     auto ld4 = [](const float* p) {
-      return kShared ? *reinterpret_cast<const float4*>(p) : __ldcg(reinterpret_cast<const float4*>(p));
+      return kOwn ? *reinterpret_cast<const float4*>(p) : __ldcg(reinterpret_cast<const float4*>(p));
     };
     for (int e = threadIdx.x; e < RB * (D / 4); e += blockDim.x) {
       const int row = e / (D / 4), d = e % (D / 4) * 4;
@@ -595,8 +704,9 @@ __global__ void __launch_bounds__(kMaxWarps * 32, 1) attend4_kernel(const Attend
   auto close = [&](int first, int last, bool from_head, long long seg, bool done) {
     // parts: the first warp's head or tail, then the heads of the warps after it
     auto part = [&](int i) -> const float* {
-      if (i == 0 && !from_head) return reinterpret_cast<const float*>(smem + (size_t)first * kStages * SB);
-      return heads_part + (size_t)(first + i) * SLOT;
+      const int w = first + i;
+      if ((i > 0 || from_head) && s_head_done[w] == 2) return a.warp_part + (size_t)(blockIdx.x * warps + w) * SLOT;
+      return reinterpret_cast<const float*>(smem + (size_t)w * (STAGES * SB));
     };
     const Cursor s = seek(seg);
     const bool left = seg < cb;  // began in an earlier CTA
@@ -660,14 +770,15 @@ int col_tiles(int R, int dtype, int D) {
   return R <= rb || D == 256 ? 1 : 2;
 }
 
-size_t smem_bytes(int warps, int D, int rows, int B) {
-  const size_t stage = (size_t)kStep * D + kStep * 4;
-  return (size_t)warps * (kStages * stage + (size_t)part_floats(rows, D) * 4) + (size_t)(B + 1) * 4;
+size_t smem_bytes(int warps, int D, int nt, int B) {
+  const size_t rows = step_rows(D);
+  return (size_t)warps * (stages_of(D, nt) * rows * (D + 4) + rows * 8) + (size_t)(B + 1) * 4;
 }
 
 }  // namespace
 
-size_t attend4_part_floats(int D) { return part_floats(16, D); }
+size_t attend4_part_floats(int D) { return part_floats(D == 256 ? 8 : 16, D); }
+int attend4_warps() { return kMaxWarps; }
 
 cudaError_t setup_attend4() {
   for (int dtype : {PROX_F32, PROX_F16, PROX_BF16})
@@ -695,16 +806,17 @@ cudaError_t launch_attend4(const prox_kv4* C, const Attend4Call& c, cudaStream_t
   a.blocks = (a.R + rb - 1) / rb;
   a.err = C->err;
   a.part = C->part;
+  a.warp_part = C->warp_part;
   a.arrived = C->arrived;
   const int per16 = c.dtype == PROX_F32 ? 4 : 8;
   a.q_vec = (reinterpret_cast<uintptr_t>(c.q) & 15) == 0 && c.q_req % per16 == 0 && c.q_tok % per16 == 0 &&
             c.q_head % per16 == 0;
-  int warps = kMaxWarps;
-  while (smem_bytes(warps, C->D, rb, c.B) > (size_t)kSmemLimit - 1024) --warps;
+  int warps = warps_of(C->D, nt);
+  while (smem_bytes(warps, C->D, nt, c.B) > (size_t)kSmemLimit - 1024) --warps;  // (large batches)
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)C->num_sms, 1, 1);
   cfg.blockDim = dim3(warps * 32, 1, 1);
-  cfg.dynamicSmemBytes = smem_bytes(warps, C->D, rb, c.B);
+  cfg.dynamicSmemBytes = smem_bytes(warps, C->D, nt, c.B);
   cfg.stream = s;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;

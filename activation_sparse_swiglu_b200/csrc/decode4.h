@@ -38,7 +38,8 @@ struct prox_kv4 {
   int pages = 0, heads = 0, page = 0, D = 0;
   int device = 0, num_sms = 0;
   int* err = nullptr;
-  float* part = nullptr;    // [2 * num_sms] partial results of split contexts
+  float* part = nullptr;       // [2 * num_sms] partial results of contexts that CTAs share
+  float* warp_part = nullptr;  // [num_sms * warps] ... that warps share
   int* arrived = nullptr;   // [num_sms] CTAs that left a part, zero between calls
   void* base = nullptr;
   size_t bytes = 0;
@@ -59,6 +60,7 @@ cudaError_t launch_kv4_read(const prox_kv4* C, const int64_t* slots, int T, void
 
 cudaError_t setup_attend4();
 size_t attend4_part_floats(int D);  // one partial result
+int attend4_warps();                // of a CTA, at most
 struct Attend4Call {
   const void* q = nullptr;
   int64_t q_req = 0, q_tok = 0, q_head = 0;  // strides in elements

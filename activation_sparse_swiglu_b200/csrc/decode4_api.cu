@@ -191,7 +191,9 @@ prox_status prox_kv4_create(uint8_t* k_codes, uint16_t* k_scales, uint8_t* v_cod
   C->D = head_dim;
   C->device = dev;
   C->num_sms = sms;
-  const size_t part = align256(2 * (size_t)sms * prox::attend4_part_floats(head_dim) * 4);
+  const size_t one = prox::attend4_part_floats(head_dim) * 4;
+  const size_t warp_part = align256((size_t)sms * prox::attend4_warps() * one);
+  const size_t part = align256(2 * (size_t)sms * one) + warp_part;
   const size_t arrived = align256((size_t)sms * 4);
   C->bytes = part + arrived + 256;
   cudaError_t e = prox::setup_attend4();
@@ -207,7 +209,8 @@ prox_status prox_kv4_create(uint8_t* k_codes, uint16_t* k_scales, uint8_t* v_cod
     return cuda_fail(e, "prox_kv4_create");
   }
   char* b = static_cast<char*>(C->base);
-  C->part = reinterpret_cast<float*>(b);
+  C->warp_part = reinterpret_cast<float*>(b);
+  C->part = reinterpret_cast<float*>(b + warp_part);
   C->arrived = reinterpret_cast<int*>(b + part);
   C->err = reinterpret_cast<int*>(b + part + arrived);
   *out_host = C;

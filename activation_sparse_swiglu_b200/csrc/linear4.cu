@@ -11,13 +11,18 @@
 // reads contiguously, and no shuffle or shared memory stands between HBM and
 // the tensor core.
 //
-// A nibble masked out of a code word is an fp16 subnormal, n 2^-24 or 16 n
-// 2^-24, so a code costs 5/8 of an instruction: x takes the factor 1/16 where
-// the nibble lies 4 bits higher, and the sum starts from -8 sum_k x, which
-// makes n the code q.  (Widening to exact integers q takes 9/8 instructions;
-// the 16-token head then ran at 0.49 of the copy bandwidth, bound by issue.)
-// The offset costs accuracy only at the level of the fp32 sums: products of up
-// to 15 |x| cancel to 7 |x|.
+// A code masked out of a word is an fp16 subnormal, n 2^-24 times its place, so
+// decoding takes logical instructions only; the other operand takes up the
+// places' factors, and the sum starts from -8 sum_k x, which makes n the code q.
+// (Widening to exact integers q takes 9 instructions for 8 codes; the 16-token
+// head then ran at 0.49 of the copy bandwidth, bound by issue.)
+// The tensor core aligns products by the exponents of their factors, which for
+// a subnormal is that of the largest one: a code n 2^-24 x has 2^-14 of a code
+// step of x left for rounding, 64 n 2^-24 x has 2^-20.  So the words hold their
+// codes where the mantissa's upper bits are (decode_words): fp32 inputs shift
+// every code there (7 instructions for 8 codes), 16-bit inputs leave half of
+// them 4 bits lower (5 instructions; 2^-16 of a code step, below the 2^-12 of
+// the result's own rounding).
 //
 // x is held in fp16, scaled by a power of two per token and group of 128 that
 // brings the group's largest magnitude to 2^14: fp16 and bf16 values keep all
@@ -106,6 +111,25 @@ __device__ __forceinline__ int range_of(int U, int u, int W) {
   return (int)(((unsigned)(u + 1) * (unsigned)W - 1) / (unsigned)U);
 }
 
+// A word holds eight codes, two of each of four fields (one per 16-bit half):
+// A in bits 6-9, B in 2-5, C in 10-13, and D in 14-15 with its upper two bits
+// in bits 0-1 of the other half, so that a rotation by 8 brings D to 6-9 and C
+// to 2-5.  r: A fragments in the order a0 (B), a1 (C), a2 (A), a3 (D).
+// ALL_HIGH: every code at 6-9 (64 n 2^-24); else B and C at 2-5 (4 n 2^-24).
+template <bool ALL_HIGH>
+__device__ __forceinline__ void decode_words(uint32_t w, uint32_t (&r)[4]) {
+  const uint32_t rot = __funnelshift_r(w, w, 8);
+  r[2] = w & 0x03C003C0u;
+  r[3] = rot & 0x03C003C0u;
+  if (ALL_HIGH) {
+    r[0] = (w << 4) & 0x03C003C0u;
+    r[1] = (w >> 4) & 0x03C003C0u;
+  } else {
+    r[0] = w & 0x003C003Cu;
+    r[1] = rot & 0x003C003Cu;
+  }
+}
+
 // The largest magnitude of 16 bytes of activations.
 template <int DT>
 __device__ __forceinline__ float top(const uint4& u) {
@@ -140,6 +164,10 @@ __global__ void __launch_bounds__(warps_of(NT) * 32, 1) linear4_kernel(const Lin
   constexpr int PARTS = DT == PROX_F32 ? 2 : 1;
   constexpr int NC = 2 / PARTS;       // tokens of a thread per column tile
   constexpr int TB = 8 * NT / PARTS;  // tokens
+  constexpr bool ALL_HIGH = PARTS == 2;
+  constexpr float kStep = ALL_HIGH ? 0x1p-18f : 0x1p-22f;  // a code step in the products
+  // x at input rows 2, 3 mod 4, whose codes stand at 6-9, against rows 0, 1
+  constexpr float kHigh = ALL_HIGH ? 1.f : 0.0625f;
   extern __shared__ __align__(16) char smem[];
   __shared__ int2 s_cut[kWarps];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -269,7 +297,7 @@ __global__ void __launch_bounds__(warps_of(NT) * 32, 1) linear4_kernel(const Lin
 #pragma unroll
       for (int o = LPG / 2; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
       if (gr >= nG) continue;
-      const float f = normaliser(mx), f16 = 0.0625f * f;
+      const float f = normaliser(mx), f16 = kHigh * f;
       float sum = 0.f;  // of the group's x as the products will see it
       char* col = s_x + (size_t)(b * PARTS) * xs + gr * 256 + (lane % LPG) * (DT == PROX_F32 ? 32 : 64);
 #pragma unroll
@@ -285,7 +313,7 @@ __global__ void __launch_bounds__(warps_of(NT) * 32, 1) linear4_kernel(const Lin
           const float2 m0 = __half22float2(l0), m1 = __half22float2(l1);
           *reinterpret_cast<uint2*>(col + xs + 8 * piece) = make_uint2(h2_bits(l0), h2_bits(l1));
           sum += (b0.x + m0.x) + (b0.y + m0.y);
-          sum = fmaf((b1.x + m1.x) + (b1.y + m1.y), 16.f, sum);
+          sum = fmaf((b1.x + m1.x) + (b1.y + m1.y), 1.f / kHigh, sum);
         } else {
           *reinterpret_cast<uint4*>(col + 16 * piece) =
               make_uint4(scale2<DT>(raw[j].x, f, f, &sum), scale2<DT>(raw[j].y, f, f16, &sum),
@@ -295,7 +323,7 @@ __global__ void __launch_bounds__(warps_of(NT) * 32, 1) linear4_kernel(const Lin
       const unsigned mask = (LPG == 8 ? 0xFFu : 0xFu) << (lane / LPG * LPG);
 #pragma unroll
       for (int o = LPG / 2; o > 0; o >>= 1) sum += __shfl_xor_sync(mask, sum, o);
-      if (lane % LPG == 0) s_nf[gr * TB + b] = make_float2(inv_pow2(f), -0x1p-21f * sum);
+      if (lane % LPG == 0) s_nf[gr * TB + b] = make_float2(inv_pow2(f), -8.f * kStep * sum);
     }
     __syncthreads();
 
@@ -358,26 +386,26 @@ __global__ void __launch_bounds__(warps_of(NT) * 32, 1) linear4_kernel(const Lin
           for (int m = 0; m < 2; ++m) {
             const uint4 w4 = w[m][i >> 1];
             uint32_t r[4];
-            spread8((i & 1) ? w4.z : w4.x, r);
+            decode_words<ALL_HIGH>((i & 1) ? w4.z : w4.x, r);
 #pragma unroll
             for (int n = 0; n < NT; ++n) {
               if (i == 0) {
                 // the lo columns of fp32 start from zero
                 const float c0 = start[n][0], c1 = PARTS == 2 ? 0.f : start[n][NC - 1];
-                mma_f16(d[m][n], r[0], r[2], r[1], r[3], xv[n].x, xv[n].y, c0, c1, c0, c1);
+                mma_f16(d[m][n], r[0], r[1], r[2], r[3], xv[n].x, xv[n].y, c0, c1, c0, c1);
               } else {
-                mma_f16(d[m][n], r[0], r[2], r[1], r[3], xv[n].x, xv[n].y);
+                mma_f16(d[m][n], r[0], r[1], r[2], r[3], xv[n].x, xv[n].y);
               }
             }
-            spread8((i & 1) ? w4.w : w4.y, r);
+            decode_words<ALL_HIGH>((i & 1) ? w4.w : w4.y, r);
 #pragma unroll
-            for (int n = 0; n < NT; ++n) mma_f16(d[m][n], r[0], r[2], r[1], r[3], xv[n].z, xv[n].w);
+            for (int n = 0; n < NT; ++n) mma_f16(d[m][n], r[0], r[1], r[2], r[3], xv[n].z, xv[n].w);
           }
         }
 #pragma unroll
         for (int m = 0; m < 2; ++m) {
           const float2 s2 = __half22float2(bits_h2(m ? scw.y : scw.x));
-          const float s[2] = {s2.x * 0x1p24f, s2.y * 0x1p24f};
+          const float s[2] = {s2.x * (1.f / kStep), s2.y * (1.f / kStep)};
 #pragma unroll
           for (int n = 0; n < NT; ++n)
 #pragma unroll
@@ -467,8 +495,7 @@ __global__ void __launch_bounds__(warps_of(NT) * 32, 1) linear4_kernel(const Lin
 }
 
 // codes [strips][G][4][32 lanes][4 words]: row h of tile m (index 2 m + h) holds
-// the steps 2h and 2h + 1 of 32 input rows; word wi of a row: see spread8's
-// order.  scales [strips][G][8][tile][2].  Channels past N hold code 8 and
+// the steps 2h and 2h + 1 of 32 input rows; a word's fields: see decode_words.  scales [strips][G][8][tile][2].  Channels past N hold code 8 and
 // scale 0.
 __global__ void linear4_pack_kernel(const uint8_t* __restrict__ codes, const __half* __restrict__ scales, int N, int G,
                                     int strips, uint32_t* __restrict__ out, __half* __restrict__ out_scales) {
@@ -482,12 +509,17 @@ __global__ void linear4_pack_kernel(const uint8_t* __restrict__ codes, const __h
       const int k0 = gr * kGroupRows + 32 * (2 * h + (wi >> 1)) + 8 * (l & 3) + 4 * (wi & 1);
       uint32_t w = 0;
 #pragma unroll
-      for (int nib = 0; nib < 8; ++nib) {
-        // nibbles 0, 4, 1, 5: row l / 4, input rows k0 .. k0 + 3; 2, 6, 3, 7: row + 8
-        const int n = strip * kStrip + 16 * m + (l >> 2) + ((nib & 2) ? 8 : 0);
-        const int k = k0 + 2 * (nib & 1) + (nib >> 2);
+      for (int f = 0; f < 8; ++f) {
+        // fields B, C, A, D of the low half, then of the high: C and D belong to
+        // row + 8, A and D to input rows k0 + 2 and k0 + 3
+        const int field = f & 3, high = f >> 2;
+        const int n = strip * kStrip + 16 * m + (l >> 2) + ((field & 1) ? 8 : 0);
+        const int k = k0 + (field >= 2 ? 2 : 0) + high;
         const uint32_t c = n < N ? (codes[(size_t)k * (N / 2) + n / 2] >> (4 * (n & 1))) & 15u : 8u;
-        w |= c << (4 * nib);
+        if (field == 3)
+          w |= high ? (c & 3) << 30 | c >> 2 : (c & 3) << 14 | (c >> 2) << 16;
+        else
+          w |= c << ((field == 0 ? 2 : field == 1 ? 10 : 6) + 16 * high);
       }
       out[i] = w;
     } else {

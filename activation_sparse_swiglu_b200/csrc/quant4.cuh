@@ -49,7 +49,9 @@ __device__ __forceinline__ void widen8(uint32_t w, uint32_t (&r)[4]) {
 // r[2] = (2, 6), 16 n 2^-24 in r[1] = (1, 5) and r[3] = (3, 7).  A nibble in the
 // low mantissa bits of an fp16 zero IS that number, so this is five logical
 // instructions for eight codes; the factor 16 goes into the other operand and
-// the offset 8 into the sum's start value.
+// the offset 8 into the sum's start value.  The tensor core aligns products by
+// their factors' exponents, a subnormal's being 2^-14: sums of n 2^-24 x are
+// held to 2^-14 of a code step of the largest x (seen: 2^-14.3).
 __device__ __forceinline__ void spread8(uint32_t w, uint32_t (&r)[4]) {
   r[0] = w & 0x000F000Fu;
   r[1] = w & 0x00F000F0u;
@@ -115,6 +117,14 @@ __device__ __forceinline__ uint32_t lds32(uint32_t addr) {
   uint32_t v;
   asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v) : "r"(addr));
   return v;
+}
+__device__ __forceinline__ uint32_t lds16(uint32_t addr) {
+  unsigned short v;
+  asm volatile("ld.shared.u16 %0, [%1];" : "=h"(v) : "r"(addr));
+  return v;
+}
+__device__ __forceinline__ void sts64(uint32_t addr, uint32_t a, uint32_t b) {
+  asm volatile("st.shared.v2.u32 [%0], {%1,%2};" ::"r"(addr), "r"(a), "r"(b) : "memory");
 }
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");

@@ -50,6 +50,9 @@ def linear4(x, codes, scales):
         tol = tol + 2.0 ** -22 * mag
     top = xd.abs().view(-1, K // 128, 128).amax(-1)
     tol = tol + 2.0 ** -38 * (top @ ((q.abs() + 16) * s.abs()).sum(1))
+    # the tensor core aligns subnormal codes at 2^-14: each of a group's 8 steps
+    # is off by up to 2^-16 (fp32 inputs 2^-20) of a code step of the largest x
+    tol = tol + 8 * 2.0 ** (-20 if x.dtype == torch.float32 else -16) * (top @ s.squeeze(1).abs())
     if x.dtype == torch.float16:
         tol = tol + 2.0 ** -24  # below fp16's normal range a step is 2^-24
     return y, tol
@@ -82,8 +85,13 @@ def attend(q, k_codes, k_scales, v_codes, v_scales, table, lens, scale):
         ids = table[b, :-(-n // page)].long()
         for h in range(Hkv if n > 0 else 0):
             ks, vs = k_scales[ids, h].flatten()[:n].double(), v_scales[ids, h].flatten()[:n].double()
-            k = unpack(k_codes[ids, h]).flatten(0, 1)[:n].double() * ks[:, None]
-            v = unpack(v_codes[ids, h]).flatten(0, 1)[:n].double() * vs[:, None]
+            kq = unpack(k_codes[ids, h]).flatten(0, 1)[:n].double()
+            vq = unpack(v_codes[ids, h]).flatten(0, 1)[:n].double()
+            k, v = kq * ks[:, None], vq * vs[:, None]
+            # for 16-bit queries the sums run over codes q + 8 and start from
+            # -8 times the other factor's sum: terms of up to |q| + 16
+            more = 0 if wide else 16
+            k_mag, v_mag = (kq.abs() + more) * ks[:, None], (vq.abs() + more) * vs[:, None]
             for i in range(Tq):
                 m = n - Tq + i + 1
                 if m <= 0:
@@ -95,17 +103,25 @@ def attend(q, k_codes, k_scales, v_codes, v_scales, table, lens, scale):
                 out[b, i, h * G:(h + 1) * G] = o
                 lse[b, i, h * G:(h + 1) * G] = torch.logsumexp(z, -1)
                 # a score: at most D / 16 tensor core steps, 2 multiplications,
-                # the difference to the maximum; fp32 queries carry 22 bits
-                t = (qd.abs() @ k[:m].abs().T * abs(scale)).amax(-1, keepdim=True)
+                # the difference to the maximum; fp32 queries carry 22 bits.  For
+                # 16-bit queries a step is off by up to 2^-14 of a code step of
+                # the largest factor (subnormal codes are aligned at 2^-14)
+                t = (qd.abs() @ k_mag[:m].T * abs(scale)).amax(-1, keepdim=True)
                 e_t = (D / 16 + 6) * 2.0 ** -23 * t
+                if not wide:
+                    e_t = e_t + (D / 16) * 2.0 ** -14 * abs(scale) * qd.abs().amax(-1, keepdim=True) * ks[:m].abs().max()
                 # a probability's weight is rounded to 11 bits (fp32: 22), ex2
-                # is good to 2^-22, the sums run over m / 32 steps, each of 2
-                # tensor core steps, and are joined at most 12 + 148 times
-                e_w = (2.0 ** -21 if wide else 2.0 ** -11) + 2.0 ** -22 + (m / 32 + 170) * 2.0 ** -23
-                mag = p @ v[:m].abs()
+                # is good to 2^-22; the sums run over steps of at most 64 rows
+                # (m / 32 bounds their number), each of at most 5 tensor core
+                # steps, and are joined at most 12 + 148 times
+                e_w = (2.0 ** -21 if wide else 2.0 ** -11) + 2.0 ** -22
+                e_s = (m / 32 + 170) * 2.0 ** -23
                 # weights below 2^-28 of the largest lose bits: 2^-39 of it each
-                floor = m * 8 * vs[:m].abs().max() * 2.0 ** -38
-                tol[b, i, h * G:(h + 1) * G] = (2 * e_t + e_w) * mag + floor + HALF_STEP[q.dtype] * o.abs()
+                floor = m * 16 * vs[:m].abs().max() * 2.0 ** -38
+                tol[b, i, h * G:(h + 1) * G] = ((2 * e_t + e_w + e_s) * (p @ v[:m].abs()) + 6 * 2.0 ** -23 * (p @ v_mag[:m])
+                                                + floor + HALF_STEP[q.dtype] * o.abs())
+                if not wide:  # 5 tensor core steps per step of rows
+                    tol[b, i, h * G:(h + 1) * G] += 5 * 2.0 ** -14 * (p @ vs[:m].abs())[:, None]
                 if q.dtype == torch.float16:
                     tol[b, i, h * G:(h + 1) * G] += 2.0 ** -24
                 lse_tol[b, i, h * G:(h + 1) * G] = (e_t.squeeze(-1) + (m / 32 + 170) * 2.0 ** -23
