@@ -53,8 +53,16 @@ namespace {
 using namespace q4;
 
 constexpr int kUnit = 32;    // cache rows that are dealt out together
+// What starting a context costs beside its rows, in units (its queries, page
+// entries and lengths are fetched, its result is written): contexts are dealt
+// out as that many units longer.  (Without it a run of empty or short contexts
+// kept one warp busy for twice as long as the others.)
+constexpr int kStartUnits = 2;
+// Units of a CTA at least: a step for every warp.  Spreading a short context
+// over more CTAs saves less than joining them costs.
+constexpr int kCtaUnits = 24;
 constexpr int kMaxWarps = 12;
-constexpr int kSmemLimit = 227 * 1024;
+constexpr int kSmemLimit = 227 * 1024 - 2048;  // dynamic, beside the joins' tables
 
 // Cache rows of a step, and steps in flight or in use per warp.
 constexpr int step_rows(int D) { return D == 256 ? 32 : 64; }
@@ -110,10 +118,19 @@ __device__ __forceinline__ uint32_t prmt(uint32_t a, uint32_t b, uint32_t sel) {
   return r;
 }
 
-// A position in the sequence of units: unit c of n of (request b, head block hb).
+// A position in the sequence of units: unit c of n of a context (request b, kv
+// head, row block).
 struct Cursor {
-  int b, hb, c, n, len;
+  int b, head, block, c, n, len;
   long long beg;  // number of unit 0
+};
+
+// A run of parts of one context that warps [first, last] of a CTA hold.
+struct Chain {
+  Cursor s;
+  int first, last;
+  bool from_head;  // the first part is the warp's head
+  bool right;      // goes on in the next CTA
 };
 
 template <int DT, int D, int NT>
@@ -142,9 +159,11 @@ __global__ void __launch_bounds__(warps_of(D, NT) * 32, 1) attend4_kernel(const 
   const uint32_t sc_at = smem_u32(smem) + warps * (STAGES * SB) + warp * (ROWS * 8);
   int* pre = reinterpret_cast<int*>(smem + (size_t)warps * (STAGES * SB + ROWS * 8));  // [B + 1]
   __shared__ long long s_scan[33];
-  __shared__ long long s_head_seg[kMaxWarps], s_tail_seg[kMaxWarps];  // first unit of the context, -1: none
-  __shared__ int s_head_done[kMaxWarps];  // 0: goes on; 1: ends with the range; 2: before it
-  __shared__ int s_last;
+  __shared__ Cursor s_head[kMaxWarps], s_tail[kMaxWarps];  // the contexts a warp has parts of
+  __shared__ int s_head_at[kMaxWarps], s_tail_at[kMaxWarps];  // 0: none; else kOpen, kDone, kEarly
+  __shared__ Chain s_chain[kMaxWarps + 1];
+  __shared__ int s_chains, s_last[2];
+  constexpr int kOpen = 1, kDone = 2, kEarly = 3;  // goes on; ends with the range; ends before it
 
   pdl_wait();
   pdl_trigger();
@@ -157,58 +176,71 @@ __global__ void __launch_bounds__(warps_of(D, NT) * 32, 1) attend4_kernel(const 
   for (int i = rlo; i < rhi; ++i) {
     const int len = c.lens[i];
     if ((len < 0 || len > max_len) && blockIdx.x == 0) atomicOr(a.err, PROX_DEVERR_LEN);
-    mine += max(1, (min(max(len, 0), max_len) + kUnit - 1) / kUnit);
+    mine += kStartUnits + max(1, (min(max(len, 0), max_len) + kUnit - 1) / kUnit);
   }
   long long total;
   long long at = block_exclusive_scan(mine, s_scan, &total);
   for (int i = rlo; i < rhi; ++i) {
     pre[i] = (int)at;
-    at += max(1, (min(max(c.lens[i], 0), max_len) + kUnit - 1) / kUnit);
+    at += kStartUnits + max(1, (min(max(c.lens[i], 0), max_len) + kUnit - 1) / kUnit);
   }
   if (threadIdx.x == 0) pre[c.B] = (int)total;
-  if (threadIdx.x < kMaxWarps) s_head_seg[threadIdx.x] = s_tail_seg[threadIdx.x] = -1;
+  if (threadIdx.x < kMaxWarps) s_head_at[threadIdx.x] = s_tail_at[threadIdx.x] = 0;
+  if (threadIdx.x == 0) s_chains = 0;
   __syncthreads();
 
   const int H = a.heads * a.blocks;
-  const long long U = total * H;
-  const int P = (int)min((long long)gridDim.x, U);  // CTAs with work
+  // Places count every context's units with its start's.
+  const long long places = total * H;
+  const int P = (int)min((long long)gridDim.x, (places + kCtaUnits - 1) / kCtaUnits);  // CTAs with work
   if ((int)blockIdx.x >= P) return;
-  const long long cb = U * blockIdx.x / P, ce = U * (blockIdx.x + 1) / P;
-  const int W = (int)min((long long)warps, ce - cb);
-  const long long wb = warp < W ? cb + (ce - cb) * warp / W : ce;
-  const long long we = warp < W ? cb + (ce - cb) * (warp + 1) / W : ce;
 
-  auto enter = [&](Cursor& s) {  // request s.b, whatever head block
-    s.n = pre[s.b + 1] - pre[s.b];
+  auto enter = [&](Cursor& s) {  // request s.b, whatever head and block
+    s.n = pre[s.b + 1] - pre[s.b] - kStartUnits;
     s.len = min(max(c.lens[s.b], 0), max_len);
   };
-  auto seek = [&](long long u) {
+  // The unit at a place: the first of its context at the places of the start
+  // and the one behind them (no part is left without a unit).
+  auto seek = [&](long long place) {
     Cursor s;
     int lo = 0, hi = c.B;
     while (hi - lo > 1) {
       const int mid = (lo + hi) >> 1;
-      if ((long long)pre[mid] * H <= u)
+      if ((long long)pre[mid] * H <= place)
         lo = mid;
       else
         hi = mid;
     }
     s.b = lo;
     enter(s);
-    const long long r = u - (long long)pre[lo] * H;
-    s.hb = (int)(r / s.n);
-    s.c = (int)(r % s.n);
-    s.beg = u - s.c;
+    const unsigned r = (unsigned)(place - (long long)pre[lo] * H), m = s.n + kStartUnits;
+    const unsigned hb = r / m;
+    s.head = hb / a.blocks;
+    s.block = hb % a.blocks;
+    s.c = max(0, (int)(r - hb * m) - kStartUnits);
+    s.beg = (long long)H * (pre[lo] - kStartUnits * lo) + (long long)hb * s.n;
     return s;
   };
+  auto unit_at = [&](long long place) {
+    if (place >= places) return (long long)H * (total - (long long)kStartUnits * c.B);
+    const Cursor s = seek(place);
+    return s.beg + s.c;
+  };
+  const long long cta0 = places * blockIdx.x / P, cta1 = places * (blockIdx.x + 1) / P;
+  const long long cb = unit_at(cta0);
+  Cursor start = seek(cta0 + (cta1 - cta0) * warp / warps);
+  const long long wb = start.beg + start.c, we = unit_at(cta0 + (cta1 - cta0) * (warp + 1) / warps);
+
   // n units on, to the next context at its end (not past the last unit)
   auto advance = [&](Cursor& s, int n) {
     if ((s.c += n) < s.n) return;
     s.beg += s.n;
     s.c = 0;
-    if (++s.hb == H) {
-      s.hb = 0;
-      if (++s.b < c.B) enter(s);
-    }
+    if (++s.block < a.blocks) return;
+    s.block = 0;
+    if (++s.head < a.heads) return;
+    s.head = 0;
+    if (++s.b < c.B) enter(s);
   };
   // units of the step at s, with `left` to the range's end
   auto units = [&](const Cursor& s, long long left) {
@@ -218,40 +250,59 @@ __global__ void __launch_bounds__(warps_of(D, NT) * 32, 1) attend4_kernel(const 
   // ---- producer: the copies of one step, the page lookups one step ahead ------
   constexpr int RPI = 32 / PIECES;  // rows of one copy instruction of the warp
   int pid[MT];
+  // whether the step's rows all lie in one page
+  auto one_page = [&](const Cursor& s, int n) {
+    return (((s.c * kUnit) ^ ((s.c + n) * kUnit - 1)) >> a.page_shift) == 0;
+  };
   auto lookup = [&](const Cursor& s, int n) {
     const int32_t* row = c.table + s.b * c.table_stride;
-    const int end = min(s.len, (s.c + n) * kUnit);
+    const int end = min(s.len, (s.c + n) * kUnit), tok0 = s.c * kUnit;
+    pid[0] = tok0 < end ? row[tok0 >> a.page_shift] : -1;
+    if (one_page(s, n)) return;
 #pragma unroll
-    for (int h = 0; h < MT; ++h) {
-      const int tok = s.c * kUnit + 16 * h;
+    for (int h = 1; h < MT; ++h) {
+      const int tok = tok0 + 16 * h;
       pid[h] = tok < end ? row[tok >> a.page_shift] : -1;
     }
   };
   const int page_mask = (1 << a.page_shift) - 1;
   const int src_at = lane / PIECES * (D / 2) + lane % PIECES * 16;
   const int k_at = k_piece<D>(lane / PIECES, lane % PIECES), v_at = v_piece<D>(lane / PIECES, lane % PIECES);
-  auto copy = [&](const Cursor& s, int n, uint32_t dst) {
-    const int end = min(s.len, (s.c + n) * kUnit), head = s.hb / a.blocks;
+  const uint16_t* const sc_src = (lane < 2 ? a.ks : a.vs) + 8 * (lane & 1);  // lanes 0-3: pieces of eight scales
+  const int sc_dst = ROWS * D + ((lane >> 1) & 1) * (ROWS * 2) + 16 * (lane & 1);
+  auto page_of = [&](int id) {
+    if ((unsigned)id < (unsigned)a.pages) return id;
+    atomicOr(a.err, PROX_DEVERR_PAGE);
+    return 0;
+  };
+  // 16 rows, h 16 rows into the stage, from row r of the cache
+  auto copy16 = [&](const uint8_t* kp, const uint8_t* vp, const uint16_t* sp, int h, uint32_t dst) {
 #pragma unroll
-    for (int h = 0; h < MT; ++h) {  // 16 rows lie in one page
-      const int tok = s.c * kUnit + 16 * h;
-      if (tok >= end) break;
-      int id = pid[h];
-      if ((unsigned)id >= (unsigned)a.pages) {
-        atomicOr(a.err, PROX_DEVERR_PAGE);
-        id = 0;
-      }
-      const int64_t r = ((int64_t)id * a.heads + head << a.page_shift) + (tok & page_mask);
+    for (int i = 0; i < 16 / RPI; ++i) {
+      cp_async16(dst + k_at + (16 * h + RPI * i) * (D / 2), kp + RPI * i * (D / 2));
+      cp_async16(dst + v_at + (ROWS + 16 * h + RPI * i) * (D / 2), vp + RPI * i * (D / 2));
+    }
+    if (lane < 4) cp_async16(dst + sc_dst + 32 * h, sp);
+  };
+  auto copy = [&](const Cursor& s, int n, uint32_t dst) {
+    const int tok0 = s.c * kUnit, end = min(s.len, (s.c + n) * kUnit);
+    if (tok0 >= end) return;
+    if (one_page(s, n)) {
+      const int64_t r = (((int64_t)page_of(pid[0]) * a.heads + s.head) << a.page_shift) + (tok0 & page_mask);
       const uint8_t* kp = a.k + r * (D / 2) + src_at;
       const uint8_t* vp = a.v + r * (D / 2) + src_at;
+      const uint16_t* sp = sc_src + r;
 #pragma unroll
-      for (int i = 0; i < 16 / RPI; ++i) {
-        cp_async16(dst + k_at + (16 * h + RPI * i) * (D / 2), kp + RPI * i * (D / 2));
-        cp_async16(dst + v_at + (ROWS + 16 * h + RPI * i) * (D / 2), vp + RPI * i * (D / 2));
-      }
-      if (lane < 4)  // two pieces of eight scales each
-        cp_async16(dst + ROWS * D + (lane >> 1) * (ROWS * 2) + 32 * h + 16 * (lane & 1),
-                   (lane < 2 ? a.ks : a.vs) + r + 8 * (lane & 1));
+      for (int h = 0; h < MT; ++h)
+        if (h < 2 * n) copy16(kp + h * 8 * D, vp + h * 8 * D, sp + 16 * h, h, dst);
+      return;
+    }
+#pragma unroll
+    for (int h = 0; h < MT; ++h) {  // 16 rows lie in one page
+      const int tok = tok0 + 16 * h;
+      if (tok >= end) break;
+      const int64_t r = (((int64_t)page_of(pid[h]) * a.heads + s.head) << a.page_shift) + (tok & page_mask);
+      copy16(a.k + r * (D / 2) + src_at, a.v + r * (D / 2) + src_at, sc_src + r, h, dst);
     }
   };
 
@@ -265,10 +316,14 @@ __global__ void __launch_bounds__(warps_of(D, NT) * 32, 1) attend4_kernel(const 
   float vscale = 1.f;          // O's power of two
 
   auto row_of = [&](int nt, int e) { return PARTS == 2 ? 4 * nt + t : 8 * nt + 2 * t + e; };
+  // New token of row r of a kv head (r < 2^20: the product with 1 / G is off by
+  // less than the half that keeps it from the next integer).
+  const float inv_g = 1.f / (float)a.G;
+  auto token_of_row = [&](int r) { return (int)(((float)r + 0.5f) * inv_g); };
   auto out_at = [&](const Cursor& s, int row) {  // element (b, i, h, 0) of row `row` of s's block, -1: none
-    const int r = s.hb % a.blocks * RB + row;
+    const int r = s.block * RB + row, i = token_of_row(r);
     if (r >= a.R) return (int64_t)-1;
-    return (((int64_t)s.b * c.Tq + r / a.G) * c.Hq + (s.hb / a.blocks) * a.G + r % a.G) * (int64_t)D;
+    return (((int64_t)s.b * c.Tq + i) * c.Hq + s.head * a.G + (r - i * a.G)) * (int64_t)D;
   };
 
   auto begin_rows = [&](const Cursor& s) {
@@ -276,14 +331,14 @@ __global__ void __launch_bounds__(warps_of(D, NT) * 32, 1) attend4_kernel(const 
     float top = 0.f;
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
-      const int r = s.hb % a.blocks * RB + (PARTS == 2 ? 4 * nt + (g >> 1) : 8 * nt + g);
-      const T* q = static_cast<const T*>(c.q) + s.b * c.q_req + (r / a.G) * c.q_tok +
-                   ((s.hb / a.blocks) * a.G + r % a.G) * c.q_head;
+      const int r = s.block * RB + (PARTS == 2 ? 4 * nt + (g >> 1) : 8 * nt + g), i0 = token_of_row(r);
+      const T* q = static_cast<const T*>(c.q) + s.b * c.q_req + i0 * c.q_tok +
+                   (s.head * a.G + (r - i0 * a.G)) * c.q_head;
 #pragma unroll
       for (int i = 0; i < KW; ++i) {
         float x[8] = {};
         const int d = D == 64 ? 16 * t + 8 * i : 32 * t + 128 * (i >> 2) + 8 * (i & 3);
-        if (r < a.R) load_vals<DT, 8>(q + d, a.q_vec, x);
+        if (r < a.R && s.len > 0) load_vals<DT, 8>(q + d, a.q_vec, x);
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
           qv[nt][8 * i + j] = x[j];
@@ -332,8 +387,8 @@ __global__ void __launch_bounds__(warps_of(D, NT) * 32, 1) attend4_kernel(const 
       }
 #pragma unroll
       for (int e = 0; e < NC; ++e) {
-        const int r = s.hb % a.blocks * RB + row_of(nt, e);
-        lim[nt][e] = r < a.R ? s.len - c.Tq + r / a.G : s.len - 1;
+        const int r = s.block * RB + row_of(nt, e);
+        lim[nt][e] = r < a.R ? s.len - c.Tq + token_of_row(r) : s.len - 1;
         mx[nt][e] = -INFINITY;
         sum[nt][e] = 0.f;
       }
@@ -605,9 +660,10 @@ __global__ void __launch_bounds__(warps_of(D, NT) * 32, 1) attend4_kernel(const 
   };
 
   // ---- the warp's range -------------------------------------------------------
-  float* warp_part = a.warp_part + (size_t)(blockIdx.x * warps + warp) * SLOT;
+  float* warp_parts = a.warp_part + (size_t)blockIdx.x * warps * SLOT;  // of parts that end early
+  auto ring_part = [&](int w) { return reinterpret_cast<float*>(smem + (size_t)w * (STAGES * SB)); };
   if (wb < we) {
-    Cursor cur = seek(wb), pro = cur;
+    Cursor cur = start, pro = cur;
     long long left = we - wb, pleft = left;  // units to compute, to copy
     int pn = units(pro, pleft);
     lookup(pro, pn);
@@ -632,23 +688,23 @@ __global__ void __launch_bounds__(warps_of(D, NT) * 32, 1) attend4_kernel(const 
       __syncwarp();
       issue(next);
       next = st;
-      step(cur, n, st);
+      if (cur.len > 0) step(cur, n, st);
       st = st == ring + (STAGES - 1) * SB ? ring : st + SB;
       left -= n;
       const bool ends = cur.c + n == cur.n;
       if (ends || left == 0) {
         float* slot = nullptr;
         if (cur.beg < wb || !ends) {  // a part; at the range's end the ring is free for it
-          slot = left > 0 ? warp_part : reinterpret_cast<float*>(smem + (size_t)warp * (STAGES * SB));
+          slot = left > 0 ? warp_parts + (size_t)warp * SLOT : ring_part(warp);
           if (left == 0) {
             cp_async_wait<0>();
             __syncwarp();
           }
           if (lane == 0) {
             if (cur.beg < wb)
-              s_head_seg[warp] = cur.beg, s_head_done[warp] = !ends ? 0 : left > 0 ? 2 : 1;
+              s_head[warp] = cur, s_head_at[warp] = !ends ? kOpen : left > 0 ? kEarly : kDone;
             else
-              s_tail_seg[warp] = cur.beg;
+              s_tail[warp] = cur, s_tail_at[warp] = kOpen;
           }
         }
         end_rows(cur, slot);
@@ -664,88 +720,151 @@ __global__ void __launch_bounds__(warps_of(D, NT) * 32, 1) attend4_kernel(const 
   __syncthreads();
 
   // ---- contexts that several warps or CTAs share -------------------------------
-  // `n` parts of one context, the i-th at part(i) (this CTA's own, or written by
-  // other CTAs): joined in order into the output, or into one part at `to`.
-  auto join = [&](auto own, int n, auto&& part, const Cursor& s, float* to) {
-    constexpr bool kOwn = decltype(own)::value;
-    auto ld1 = [](const float* p) { return kOwn ? *p : __ldcg(p); };
-    auto ld4 = [](const float* p) {
-      return kOwn ? *reinterpret_cast<const float4*>(p) : __ldcg(reinterpret_cast<const float4*>(p));
+  // A chain ends where a head is done, or with the CTA's last warp that has a
+  // part; it begins at the tail before it, or with the CTA's first part.
+  if (lane == 0) {
+    auto add = [&](const Cursor& s, int last, bool tail_only, bool right) {
+      int f = last;
+      bool from_head = !tail_only;
+      while (from_head && f > 0) {
+        int p = f - 1;  // the warp before it with a part
+        while (p >= 0 && !s_head_at[p] && !s_tail_at[p]) --p;
+        if (p < 0) break;
+        from_head = !s_tail_at[p];
+        if (from_head && s_head_at[p] != kOpen) {  // that head is of another context
+          from_head = true;
+          break;
+        }
+        f = p;
+      }
+      Chain& ch = s_chain[atomicAdd(&s_chains, 1)];
+      ch.s = s;
+      ch.first = f;
+      ch.last = last;
+      ch.from_head = from_head;
+      ch.right = right;
     };
-    for (int e = threadIdx.x; e < RB * (D / 4); e += blockDim.x) {
+    bool more = false;  // a later warp has a head
+    for (int w = warp + 1; w < warps; ++w) more |= s_head_at[w] != 0;
+    if (s_head_at[warp] >= kDone) add(s_head[warp], warp, false, false);
+    if (s_head_at[warp] == kOpen && !more) add(s_head[warp], warp, false, true);
+    if (s_tail_at[warp] && !more) add(s_tail[warp], warp, true, true);
+  }
+  __syncthreads();
+  const int chains = s_chains;
+  if (chains == 0) return;
+  constexpr int kSlices = RB * (D / 4);  // of four values, of a part
+  // parts added one by one to a row's maximum, sum and four values
+  auto result = [&](const Cursor& s, int row, int d, float top, float l, float(&y)[4], float* to) {
+    if (to) {
+      store_vals<PROX_F32, 4>(to + row * D + d, true, y);
+      if (d == 0) to[RB * D + row] = top, to[RB * D + RB + row] = l;
+      return;
+    }
+    const int64_t o = out_at(s, row);
+    if (o < 0) return;
+    const float f = l == 0.f ? 0.f : 1.f / l;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) y[i] *= f;
+    store_vals<DT, 4>(static_cast<T*>(c.out) + o + d, true, y);
+    if (c.lse && d == 0) c.lse[o / D] = l == 0.f ? -INFINITY : 0.6931471805599453f * (top + log2f(l));
+  };
+  for (int e = threadIdx.x; e < chains * kSlices; e += blockDim.x) {
+    const Chain& ch = s_chain[e / kSlices];
+    const int row = e % kSlices / (D / 4), d = e % (D / 4) * 4;
+    auto part = [&](int w) -> const float* {  // the chain's part in warp w, NULL: none
+      if (w == ch.first && !ch.from_head) return ring_part(w);
+      if (!s_head_at[w]) return nullptr;
+      return s_head_at[w] == kEarly ? warp_parts + (size_t)w * SLOT : ring_part(w);
+    };
+    // (four parts' loads at once: some lie in global memory)
+    float top = -INFINITY, l = 0.f, y[4] = {};
+    for (int w0 = ch.first; w0 <= ch.last; w0 += 4) {
+      const float* p[4];
+      float m[4], q[4];
+      float4 o[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        p[i] = w0 + i <= ch.last ? part(w0 + i) : nullptr;
+        m[i] = p[i] ? p[i][RB * D + row] : -INFINITY;
+        q[i] = p[i] ? p[i][RB * D + RB + row] : 0.f;
+        o[i] = p[i] ? *reinterpret_cast<const float4*>(p[i] + row * D + d) : make_float4(0.f, 0.f, 0.f, 0.f);
+      }
+      const float up = fmaxf(fmaxf(fmaxf(m[0], m[1]), fmaxf(m[2], m[3])), top);
+      const float base = up == -INFINITY ? 0.f : up;
+      float f = exp2_fast(top - base);
+      top = up;
+      l *= f;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) y[i] *= f;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        f = exp2_fast(m[i] - base);  // 0 where there is no part
+        l = fmaf(q[i], f, l);
+        y[0] = fmaf(o[i].x, f, y[0]), y[1] = fmaf(o[i].y, f, y[1]);
+        y[2] = fmaf(o[i].z, f, y[2]), y[3] = fmaf(o[i].w, f, y[3]);
+      }
+    }
+    const bool left = ch.s.beg < cb;  // began in an earlier CTA
+    result(ch.s, row, d, top, l, y,
+           left || ch.right ? a.part + (size_t)(2 * blockIdx.x + (left ? 0 : 1)) * SLOT : nullptr);
+  }
+  bool shared = false;
+  for (int i = 0; i < chains; ++i) shared |= s_chain[i].right || s_chain[i].s.beg < cb;
+  if (!shared) return;
+  // the last CTA to leave its part of a context joins them all
+  __threadfence();
+  __syncthreads();
+  auto ctas = [&](const Cursor& s, int* c0, int* c1) {
+    const long long first = (long long)H * pre[s.b] + (long long)(s.head * a.blocks + s.block) * (s.n + kStartUnits) +
+                            kStartUnits;  // the place behind the context's start
+    *c0 = (int)(((first + 1) * P - 1) / places);
+    *c1 = (int)(((first + s.n) * P - 1) / places);
+  };
+  if (threadIdx.x < 2) {  // the context from the left, the one that goes on to the right
+    int found = -1;
+    for (int i = 0; i < chains; ++i) {
+      const bool left = s_chain[i].s.beg < cb;
+      if (threadIdx.x == 0 ? left : !left && s_chain[i].right) found = i;
+    }
+    if (found >= 0) {
+      int c0, c1;
+      ctas(s_chain[found].s, &c0, &c1);
+      if (atomicAdd(a.arrived + c0, 1) == c1 - c0)
+        a.arrived[c0] = 0;  // for the next call
+      else
+        found = -1;
+    }
+    s_last[threadIdx.x] = found;
+  }
+  __syncthreads();
+#pragma unroll
+  for (int k = 0; k < 2; ++k) {
+    if (s_last[k] < 0) continue;
+    __threadfence();
+    const Cursor s = s_chain[s_last[k]].s;
+    int c0, c1;
+    ctas(s, &c0, &c1);
+    auto part = [&](int cta) { return a.part + (size_t)(2 * cta + (cta == c0 ? 1 : 0)) * SLOT; };
+    for (int e = threadIdx.x; e < kSlices; e += blockDim.x) {
       const int row = e / (D / 4), d = e % (D / 4) * 4;
       float top = -INFINITY;
-      for (int i = 0; i < n; ++i) top = fmaxf(top, ld1(part(i) + RB * D + row));
+#pragma unroll 8
+      for (int i = c0; i <= c1; ++i) top = fmaxf(top, __ldcg(part(i) + RB * D + row));
       const float base = top == -INFINITY ? 0.f : top;
-      float l = 0.f;
-      float y[4] = {};
-      for (int i = 0; i < n; ++i) {
+      float l = 0.f, y[4] = {};
+#pragma unroll 4
+      for (int i = c0; i <= c1; ++i) {
         const float* p = part(i);
-        const float f = exp2_fast(ld1(p + RB * D + row) - base);
-        l = fmaf(ld1(p + RB * D + RB + row), f, l);
-        const float4 o = ld4(p + row * D + d);
+        const float f = exp2_fast(__ldcg(p + RB * D + row) - base);
+        const float4 o = __ldcg(reinterpret_cast<const float4*>(p + row * D + d));
+        l = fmaf(__ldcg(p + RB * D + RB + row), f, l);
         y[0] = fmaf(o.x, f, y[0]), y[1] = fmaf(o.y, f, y[1]);
         y[2] = fmaf(o.z, f, y[2]), y[3] = fmaf(o.w, f, y[3]);
       }
-      if (to) {
-        store_vals<PROX_F32, 4>(to + row * D + d, true, y);
-        if (d == 0) to[RB * D + row] = top, to[RB * D + RB + row] = l;
-        continue;
-      }
-      const int64_t o = out_at(s, row);
-      if (o < 0) continue;
-      const float f = l == 0.f ? 0.f : 1.f / l;
-#pragma unroll
-      for (int i = 0; i < 4; ++i) y[i] *= f;
-      store_vals<DT, 4>(static_cast<T*>(c.out) + o + d, true, y);
-      if (c.lse && d == 0) c.lse[o / D] = l == 0.f ? -INFINITY : 0.6931471805599453f * (top + log2f(l));
+      result(s, row, d, top, l, y, nullptr);
     }
-  };
-  auto close = [&](int first, int last, bool from_head, long long seg, bool done) {
-    // parts: the first warp's head or tail, then the heads of the warps after it
-    auto part = [&](int i) -> const float* {
-      const int w = first + i;
-      if ((i > 0 || from_head) && s_head_done[w] == 2) return a.warp_part + (size_t)(blockIdx.x * warps + w) * SLOT;
-      return reinterpret_cast<const float*>(smem + (size_t)w * (STAGES * SB));
-    };
-    const Cursor s = seek(seg);
-    const bool left = seg < cb;  // began in an earlier CTA
-    if (!left && done) {
-      join(std::true_type(), last - first + 1, part, s, nullptr);
-      return;
-    }
-    float* to = a.part + (size_t)(2 * blockIdx.x + (left ? 0 : 1)) * SLOT;
-    join(std::true_type(), last - first + 1, part, s, to);
-    __threadfence();
-    __syncthreads();
-    const int c0 = (int)(((seg + 1) * P - 1) / U), c1 = (int)(((seg + s.n) * P - 1) / U);
-    if (threadIdx.x == 0) {
-      const int n = atomicAdd(a.arrived + c0, 1);
-      s_last = n == c1 - c0;
-      if (s_last) a.arrived[c0] = 0;  // for the next call
-    }
-    __syncthreads();
-    if (s_last) {
-      __threadfence();
-      join(std::false_type(), c1 - c0 + 1,
-           [&](int i) -> const float* { return a.part + (size_t)(2 * (c0 + i) + (i == 0 ? 1 : 0)) * SLOT; }, s,
-           nullptr);
-    }
-  };
-  int first = -1;
-  bool from_head = false;
-  long long seg = -1;
-  for (int w = 0; w < W; ++w) {
-    if (s_head_seg[w] >= 0) {
-      if (first < 0) first = w, from_head = true, seg = s_head_seg[w];
-      if (s_head_done[w]) {
-        close(first, w, from_head, seg, true);
-        first = -1;
-      }
-    }
-    if (s_tail_seg[w] >= 0) first = w, from_head = false, seg = s_tail_seg[w];
   }
-  if (first >= 0) close(first, W - 1, from_head, seg, false);
 }
 
 using Kernel = void (*)(const AttendArgs);
@@ -785,7 +904,7 @@ cudaError_t setup_attend4() {
     for (int D : {64, 128, 256})
       for (int nt : {1, 2}) {
         cudaError_t e =
-            cudaFuncSetAttribute(pick(dtype, D, nt), cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemLimit - 1024);
+            cudaFuncSetAttribute(pick(dtype, D, nt), cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemLimit);
         if (e != cudaSuccess) return e;
       }
   return cudaSuccess;
@@ -812,7 +931,7 @@ cudaError_t launch_attend4(const prox_kv4* C, const Attend4Call& c, cudaStream_t
   a.q_vec = (reinterpret_cast<uintptr_t>(c.q) & 15) == 0 && c.q_req % per16 == 0 && c.q_tok % per16 == 0 &&
             c.q_head % per16 == 0;
   int warps = warps_of(C->D, nt);
-  while (smem_bytes(warps, C->D, nt, c.B) > (size_t)kSmemLimit - 1024) --warps;  // (large batches)
+  while (smem_bytes(warps, C->D, nt, c.B) > (size_t)kSmemLimit) --warps;  // (large batches)
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)C->num_sms, 1, 1);
   cfg.blockDim = dim3(warps * 32, 1, 1);

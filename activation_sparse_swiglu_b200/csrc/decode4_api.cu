@@ -286,6 +286,8 @@ prox_status prox_kv4_attend(const prox_kv4* C, const void* q, int64_t q_req, int
   if (Tq < 1 || (int64_t)Tq * n_q_heads > (1 << 20))
     return fail(PROX_EINVAL, "Tq=%d must be positive and Tq * n_q_heads at most 2^20", Tq);
   if (cols < 0 || table_stride < cols) return fail(PROX_EINVAL, "cols=%d must be >= 0 and table_stride >= cols", cols);
+  if (((int64_t)cols * C->page / 32 + 3) * Tq * n_q_heads >= (int64_t)1 << 32)
+    return fail(PROX_EINVAL, "cols * page_size * Tq * n_q_heads must stay below 2^36");
   if (!std::isfinite(scale)) return fail(PROX_EINVAL, "scale must be finite");
   if (!q || !aligned(q, dtype_size(dtype)) || !out || !aligned16(out))
     return fail(PROX_EINVAL, "q must be aligned to its type and out a 16-byte aligned pointer");
