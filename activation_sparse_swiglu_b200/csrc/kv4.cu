@@ -5,13 +5,16 @@
 // contiguous over its lanes): the largest magnitude by shuffles, the scale
 // S = fp16(amax / 7), and the codes.
 //
-// The code of x is x / S rounded half to even, exactly: n = rint(x * (1 / S))
-// is off by at most one, and e = x - n S is exact in one fused multiply-add
-// (n S has at most 15 significant bits, and |e| < S is a multiple of both
-// numbers' units), so comparing |e| with S / 2 settles n, ties included.
+// The code of x is x / S rounded half to even, exactly.  The quotient q is
+// corrected once by its exact remainder, so it is right where it is a number of
+// 24 bits, ties n + 1/2 among them.  For 16-bit x nothing else can go wrong: x / S
+// off a tie is off it by 2^-12 at least (both are integers of 11 bits times
+// powers of two).  For fp32 x a quotient next to a tie may have been rounded
+// onto it: e = x - n S, exact in one fused multiply-add, then exceeds S / 2.
+// Adding 1.5 2^23 + 8 rounds q and leaves the code in the low bits.
 //
-// Bound: HBM for prompts (16000 tokens x 8 heads of 128: 65 MB in, 17 MB
-// out); launch latency for the rows of a decode step.
+// Bound: HBM for prompts (16000 tokens x 8 heads of 128: 65 MB in, 17 MB out),
+// with issue close behind; launch latency for the rows of a decode step.
 #include <type_traits>
 
 #include "decode4.h"
@@ -24,17 +27,38 @@ using namespace q4;
 
 constexpr int kThreads = 256;
 
-__device__ __forceinline__ uint32_t code8(const float (&x)[8], float s) {
-  const float half = 0.5f * s, rs = 1.0f / s;
+// Eight codes of x under a scale s whose quotients all lie within 7.5.
+template <int DT>
+__device__ __forceinline__ uint32_t code8(const float (&x)[8], float s, float rs, float half) {
+  constexpr float kMagic = 12582912.f + 8.f;
   uint32_t w = 0;
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    float n = rintf(x[i] * rs);
-    const float e = fmaf(-n, s, x[i]), a = fabsf(e);
-    if (a >= half && (a > half || (((int)n) & 1))) n += copysignf(1.f, e);
-    // s > 0 and finite: n is finite; a NaN or infinity in x gave s = NaN or inf
-    const int q = s > 0.f ? (int)fminf(fmaxf(n, -7.f), 7.f) : 0;
-    w |= (uint32_t)(q + 8) << (4 * i);
+  for (int i = 7; i >= 0; --i) {
+    const float q0 = x[i] * rs;
+    const float q = fmaf(fmaf(-q0, s, x[i]), rs, q0);
+    float t = q + kMagic;
+    if (DT == PROX_F32) {
+      const float e = fmaf(-(t - kMagic), s, x[i]);
+      if (fabsf(e) > half) t += copysignf(1.f, e);
+    }
+    w = w * 16 + (__float_as_uint(t) & 15u);
+  }
+  return w;
+}
+// The same for any scale: 0 (codes 0), infinite or NaN (codes 0; the row reads
+// as NaN), and fp16's subnormals, whose coarse steps leave quotients past 7.
+__device__ uint32_t code8_any(const float (&x)[8], float s) {
+  uint32_t w = 0;
+  for (int i = 7; i >= 0; --i) {
+    int n = 0;
+    if (s > 0.f && s <= 65504.f) {
+      const float q = x[i] / s;
+      n = (int)rintf(q);
+      const float e = fmaf(-(float)n, s, x[i]);
+      if (fabsf(e) > 0.5f * s) n += e > 0.f ? 1 : -1;
+      n = min(7, max(-7, n));
+    }
+    w = w * 16 + (uint32_t)(n + 8);
   }
   return w;
 }
@@ -42,24 +66,24 @@ __device__ __forceinline__ uint32_t code8(const float (&x)[8], float s) {
 template <int DT, int D>
 __global__ void __launch_bounds__(kThreads) append_kernel(prox_kv4 C, const void* k_in, const void* v_in,
                                                           int64_t k_token, int64_t k_head, int64_t v_token,
-                                                          int64_t v_head, const int64_t* slots, int T, bool vec) {
+                                                          int64_t v_head, const int64_t* slots, int T, int shift, bool vec) {
   using T_ = typename Act<DT>::T;
   constexpr int LPR = D / 16;  // lanes of one row
   pdl_wait();
   pdl_trigger();
   const int lane = threadIdx.x % LPR;
-  const int64_t row = ((int64_t)blockIdx.x * kThreads + threadIdx.x) / LPR;
+  const unsigned row = (unsigned)(((int64_t)blockIdx.x * kThreads + threadIdx.x) / LPR);
   const bool is_v = blockIdx.y;
-  if (row / C.heads >= T) return;  // a whole row's lanes leave together
-  const int t = (int)(row / C.heads), h = (int)(row % C.heads);
+  const unsigned t = row / (unsigned)C.heads, h = row - t * C.heads;
+  if (t >= (unsigned)T) return;  // a whole row's lanes leave together
   const int64_t slot = slots[t];
   if (slot < 0) return;
   if (slot >= (int64_t)C.pages * C.page) {
     if (lane == 0) atomicOr(C.err, PROX_DEVERR_SLOT);
     return;
   }
-  const T_* x = static_cast<const T_*>(is_v ? v_in : k_in) + t * (is_v ? v_token : k_token) +
-                h * (is_v ? v_head : k_head);
+  const T_* x = static_cast<const T_*>(is_v ? v_in : k_in) + (int64_t)t * (is_v ? v_token : k_token) +
+                (int64_t)h * (is_v ? v_head : k_head);
   float a[8], b[8];
   load_vals<DT, 8>(x + 8 * lane, vec, a);
   load_vals<DT, 8>(x + D / 2 + 8 * lane, vec, b);
@@ -71,22 +95,50 @@ __global__ void __launch_bounds__(kThreads) append_kernel(prox_kv4 C, const void
   for (int o = LPR / 2; o > 0; o >>= 1) mx = max_nan(mx, __shfl_xor_sync(mask, mx, o));
   const __half sh = __float2half_rn(mx / 7.0f);
   const float s = __half2float(sh);
-  const int64_t page = slot / C.page, r = slot % C.page;
-  const int64_t at = (page * C.heads + h) * C.page + r;
+  const int64_t at = (((slot >> shift) * C.heads + h) << shift) + (slot & (C.page - 1));
   uint8_t* dst = (is_v ? C.v : C.k) + at * (D / 2);
-  *reinterpret_cast<uint32_t*>(dst + 4 * lane) = code8(a, s);
-  *reinterpret_cast<uint32_t*>(dst + D / 4 + 4 * lane) = code8(b, s);
+  uint32_t ca, cb;
+  if (s >= 0x1p-14f && s <= 65504.f) {
+    const float rs = 1.0f / s, half = 0.5f * s;
+    ca = code8<DT>(a, s, rs, half);
+    cb = code8<DT>(b, s, rs, half);
+  } else {
+    ca = code8_any(a, s);
+    cb = code8_any(b, s);
+  }
+  *reinterpret_cast<uint32_t*>(dst + 4 * lane) = ca;
+  *reinterpret_cast<uint32_t*>(dst + D / 4 + 4 * lane) = cb;
   if (lane == 0) reinterpret_cast<__half*>(is_v ? C.vs : C.ks)[at] = sh;
 }
 
-__device__ __forceinline__ void value8(uint32_t w, float s, float (&v)[8]) {
+// The eight values of a word under scale s, rounded once and stored.  (A code
+// times an fp16 scale has 15 significant bits: one rounding in any type.)
+template <int DT>
+__device__ __forceinline__ void store8(typename Act<DT>::T* y, uint32_t w, __half s) {
+  uint32_t r[4];  // nibbles (0, 4), (1, 5), (2, 6), (3, 7)
+  widen8(w, r);
+  if constexpr (DT == PROX_F16) {
+    const __half2 s2 = __half2half2(s);
 #pragma unroll
-  for (int i = 0; i < 8; ++i) v[i] = (float)((int)((w >> (4 * i)) & 15u) - 8) * s;
+    for (int i = 0; i < 4; ++i) r[i] = h2_bits(__hmul2(bits_h2(r[i]), s2));
+    *reinterpret_cast<uint4*>(y) =
+        make_uint4(__byte_perm(r[0], r[1], 0x5410), __byte_perm(r[2], r[3], 0x5410), __byte_perm(r[0], r[1], 0x7632),
+                   __byte_perm(r[2], r[3], 0x7632));
+  } else {
+    const float f = __half2float(s);
+    float v[8];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float2 q = __half22float2(bits_h2(r[i]));
+      v[i] = q.x * f, v[4 + i] = q.y * f;
+    }
+    store_vals<DT, 8>(y, true, v);
+  }
 }
 
 template <int DT, int D>
-__global__ void __launch_bounds__(kThreads) read_kernel(prox_kv4 C, const int64_t* slots, int T, void* k_out,
-                                                        void* v_out) {
+__global__ void __launch_bounds__(kThreads) read_kernel(prox_kv4 C, const int64_t* slots, int T, int shift,
+                                                        void* k_out, void* v_out) {
   using T_ = typename Act<DT>::T;
   constexpr int LPR = D / 16;
   pdl_wait();
@@ -97,19 +149,26 @@ __global__ void __launch_bounds__(kThreads) read_kernel(prox_kv4 C, const int64_
   if (row / C.heads >= T) return;
   const int t = (int)(row / C.heads), h = (int)(row % C.heads);
   const int64_t slot = slots[t];
-  float a[8] = {}, b[8] = {};
+  T_* y = static_cast<T_*>(is_v ? v_out : k_out) + (int64_t)row * D;
+  uint32_t wa = 0x88888888u, wb = wa;
+  __half sc = __half(0.f);
   if (slot >= (int64_t)C.pages * C.page) {
     if (lane == 0) atomicOr(C.err, PROX_DEVERR_SLOT);
   } else if (slot >= 0) {
-    const int64_t at = ((slot / C.page) * C.heads + h) * C.page + slot % C.page;
+    const int64_t at = (((slot >> shift) * C.heads + h) << shift) + (slot & (C.page - 1));
     const uint8_t* src = (is_v ? C.v : C.k) + at * (D / 2);
-    const float s = __half2float(reinterpret_cast<const __half*>(is_v ? C.vs : C.ks)[at]);
-    value8(*reinterpret_cast<const uint32_t*>(src + 4 * lane), s, a);
-    value8(*reinterpret_cast<const uint32_t*>(src + D / 4 + 4 * lane), s, b);
+    sc = reinterpret_cast<const __half*>(is_v ? C.vs : C.ks)[at];
+    wa = *reinterpret_cast<const uint32_t*>(src + 4 * lane);
+    wb = *reinterpret_cast<const uint32_t*>(src + D / 4 + 4 * lane);
   }
-  T_* y = static_cast<T_*>(is_v ? v_out : k_out) + row * D;
-  store_vals<DT, 8>(y + 8 * lane, true, a);
-  store_vals<DT, 8>(y + D / 2 + 8 * lane, true, b);
+  store8<DT>(y + 8 * lane, wa, sc);
+  store8<DT>(y + D / 2 + 8 * lane, wb, sc);
+}
+
+int shift_of(int page) {
+  int s = 0;
+  while ((1 << s) < page) ++s;
+  return s;
 }
 
 cudaLaunchConfig_t rows_config(int64_t rows, int lanes, cudaStream_t s, cudaLaunchAttribute* attr) {
@@ -153,7 +212,7 @@ cudaError_t launch_kv4_append(const prox_kv4* C, const void* k, const void* v, i
     cudaLaunchAttribute attr[1];
     cudaLaunchConfig_t cfg = rows_config((int64_t)T * C->heads, C->D / 16, s, attr);
     return cudaLaunchKernelEx(&cfg, append_kernel<decltype(dt)::value, decltype(d)::value>, *C, k, v, k_token, k_head,
-                              v_token, v_head, slots, T, vec);
+                              v_token, v_head, slots, T, shift_of(C->page), vec);
   });
 }
 
@@ -162,7 +221,8 @@ cudaError_t launch_kv4_read(const prox_kv4* C, const int64_t* slots, int T, void
   return by_shape(dtype, C->D, [&](auto dt, auto d) {
     cudaLaunchAttribute attr[1];
     cudaLaunchConfig_t cfg = rows_config((int64_t)T * C->heads, C->D / 16, s, attr);
-    return cudaLaunchKernelEx(&cfg, read_kernel<decltype(dt)::value, decltype(d)::value>, *C, slots, T, k, v);
+    return cudaLaunchKernelEx(&cfg, read_kernel<decltype(dt)::value, decltype(d)::value>, *C, slots, T,
+                              shift_of(C->page), k, v);
   });
 }
 

@@ -83,6 +83,8 @@ __global__ void __launch_bounds__(1024) page_plan_kernel(PagePlan p, int ctas) {
   }
   __syncthreads();
   const int total = bad ? 0 : (int)all_new;
+  int top_step = 1;
+  while (2 * top_step < p.B) top_step *= 2;
   const int all = gridDim.x * blockDim.x, at = blockIdx.x * blockDim.x + tid;
   if (!bad) {
     for (int n = at; n < returned; n += all) {
@@ -103,17 +105,32 @@ __global__ void __launch_bounds__(1024) page_plan_kernel(PagePlan p, int ctas) {
     cluster_sync_all();
   else
     __syncthreads();
-  for (int n = at; n < p.max_new; n += all) {
-    long long slot = -1;
-    int pos = -1;
-    if (n < total) {
-      const int i = find_row(s_new, p.B, n);
-      pos = s_len[i] + (n - s_new[i]);
-      const int col = pos / p.page;
-      slot = (long long)__ldcg(p.table + (size_t)i * p.table_stride + col) * p.page + (pos - col * p.page);
+  // four tokens of a thread at once: their searches and page loads overlap
+  for (int n0 = at; n0 < p.max_new; n0 += 4 * all) {
+    int row[4], pos[4], id[4], col[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) row[k] = 0;
+    for (int step = top_step; step > 0; step >>= 1)  // the largest i with s_new[i] <= n
+#pragma unroll
+      for (int k = 0; k < 4; ++k)
+        if (row[k] + step < p.B && s_new[row[k] + step] <= n0 + k * all) row[k] += step;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const int n = n0 + k * all;
+      pos[k] = -1;
+      if (n < total) {
+        pos[k] = s_len[row[k]] + (n - s_new[row[k]]);
+        col[k] = pos[k] / p.page;
+        id[k] = __ldcg(p.table + (size_t)row[k] * p.table_stride + col[k]);
+      }
     }
-    p.slots[n] = slot;
-    p.positions[n] = pos;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const int n = n0 + k * all;
+      if (n >= p.max_new) break;
+      p.slots[n] = pos[k] < 0 ? -1 : (long long)id[k] * p.page + (pos[k] - col[k] * p.page);
+      p.positions[n] = pos[k];
+    }
   }
   for (int i = at; i <= p.B; i += all) p.cu[i] = bad ? 0 : s_new[i];
   // delta is still read here, so lens_out may be lens but not delta
