@@ -321,7 +321,7 @@ prox_status prox_plan_pages(const int32_t* lens, const int32_t* delta, int B, in
                             int64_t* slots, int32_t* positions, int max_new, int32_t* status, void* stream) {
   if (B < 1 || B > prox::kPlanMaxRequests)
     return fail(PROX_EINVAL, "B=%d must be in [1, %d]", B, prox::kPlanMaxRequests);
-  if (page_size < 1) return fail(PROX_EINVAL, "page_size=%d must be positive", page_size);
+  if (page_size < 1 || page_size > 1 << 30) return fail(PROX_EINVAL, "page_size=%d must be in [1, 2^30]", page_size);
   if (cols < 0 || table_stride < cols || (int64_t)B * cols > INT_MAX)
     return fail(PROX_EINVAL, "cols=%d must be >= 0, table_stride >= cols and B * cols < 2^31", cols);
   if (free_cap < 0 || max_new < 0) return fail(PROX_EINVAL, "free_cap and max_new must be >= 0");

@@ -23,41 +23,50 @@ from ._lib import DTYPE_BF16, DTYPE_F16, DTYPE_F32, check, lib
 DTYPES = {torch.float32: DTYPE_F32, torch.float16: DTYPE_F16, torch.bfloat16: DTYPE_BF16}
 
 
-def _raw_stream(stream, device: torch.device) -> int:
+def _raw_stream(stream, index: int) -> int:
     if stream is None:
-        return torch._C._cuda_getCurrentRawStream(device.index)
+        return torch._C._cuda_getCurrentRawStream(index)
     return stream.cuda_stream if isinstance(stream, torch.cuda.Stream) else int(stream)
 
 
-def _empty(shape, dtype, device, stream) -> torch.Tensor:
-    """A result tensor that belongs to the stream that writes it."""
-    if isinstance(stream, torch.cuda.Stream):
+def _empty(like: torch.Tensor, shape, dtype, stream) -> torch.Tensor:
+    """A result tensor on like's device that belongs to the stream that writes it."""
+    if stream is not None and isinstance(stream, torch.cuda.Stream):
         with torch.cuda.stream(stream):
-            return torch.empty(shape, dtype=dtype, device=device)
-    return torch.empty(shape, dtype=dtype, device=device)
+            return like.new_empty(shape, dtype=dtype)
+    return like.new_empty(shape, dtype=dtype)
 
 
 def _act(t: torch.Tensor, name: str) -> int:
+    """The library's code of t's type."""
+    code = DTYPES.get(t.dtype) if isinstance(t, torch.Tensor) and t.is_cuda else None
+    if code is not None:
+        return code
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise TypeError(f"{name} must be a CUDA tensor")
-    code = DTYPES.get(t.dtype)
-    if code is None:
-        raise TypeError(f"{name} must be float32, float16 or bfloat16, got {t.dtype}")
-    return code
+    raise TypeError(f"{name} must be float32, float16 or bfloat16, got {t.dtype}")
 
 
-def _ints(t: torch.Tensor, dtype: torch.dtype, numel: int, name: str) -> torch.Tensor:
+def _ints(t: torch.Tensor, dtype: torch.dtype, numel: int, name: str) -> None:
     if not isinstance(t, torch.Tensor) or not t.is_cuda or t.dtype != dtype:
         raise TypeError(f"{name} must be a CUDA tensor of {dtype}")
     if t.numel() != numel or not t.is_contiguous():
         raise ValueError(f"{name} must hold {numel} contiguous values")
-    return t
 
 
-def _same_device(device: torch.device, **tensors) -> None:
-    for name, t in tensors.items():
-        if t is not None and t.device != device:
-            raise ValueError(f"{name} is on {t.device}, not on {device}")
+def _on(index: int, t: torch.Tensor, name: str) -> None:
+    if t.get_device() != index:
+        raise ValueError(f"{name} is on {t.device}, not on cuda:{index}")
+
+
+def _table(t: torch.Tensor, rows: int) -> tuple[int, int]:
+    """(columns, row stride) of a page table."""
+    if not isinstance(t, torch.Tensor) or t.dtype != torch.int32 or t.dim() != 2:
+        raise ValueError(f"table must be int32 [{rows}, cols] with contiguous rows")
+    (n, cols), (step, one) = t.shape, t.stride()
+    if n != rows or (cols > 1 and one != 1):
+        raise ValueError(f"table must be int32 [{rows}, cols] with contiguous rows")
+    return cols, step if step > cols else cols
 
 
 class Linear4:
@@ -81,7 +90,7 @@ class Linear4:
                 raise ValueError("w must be a contiguous [d_in, d_out] matrix")
             self._on_device(w)
             d_in, d_out = w.shape
-            check(lib.prox_linear4_create_bf16(w.data_ptr(), d_in, d_out, _raw_stream(stream, w.device),
+            check(lib.prox_linear4_create_bf16(w.data_ptr(), d_in, d_out, _raw_stream(stream, w.device.index),
                                                ctypes.byref(h)))
             self.device = w.device
         else:
@@ -97,9 +106,10 @@ class Linear4:
             if d_in % 128 or tuple(scales.shape) != (d_in // 128, d_out):
                 raise ValueError(f"scales must be [{d_in} / 128, {d_out}], got {tuple(scales.shape)}")
             check(lib.prox_linear4_create(codes.data_ptr(), scales.data_ptr(), d_in, d_out,
-                                          _raw_stream(stream, codes.device), ctypes.byref(h)))
+                                          _raw_stream(stream, codes.device.index), ctypes.byref(h)))
             self.device = codes.device
         self.d_in, self.d_out = d_in, d_out
+        self._index = self.device.index
         self._h = h
 
     @staticmethod
@@ -128,24 +138,25 @@ class Linear4:
     def forward(self, x: torch.Tensor, out: torch.Tensor | None = None, stream=None) -> torch.Tensor:
         """x [B, d_in] or [d_in] (rows may be strided) -> [B, d_out] or [d_out] of x's type."""
         dt = _act(x, "x")
-        dim = x.dim()
-        if dim not in (1, 2) or x.shape[-1] != self.d_in or x.stride(-1) != 1:
+        index, shape, strides = self._index, x.shape, x.stride()
+        dim = len(shape)
+        if dim not in (1, 2) or shape[-1] != self.d_in or strides[-1] != 1:
             raise ValueError(f"x must be [B, {self.d_in}] or [{self.d_in}] with contiguous rows, "
-                             f"got {tuple(x.shape)}")
-        B = x.shape[0] if dim == 2 else 1
+                             f"got {tuple(shape)}")
+        _on(index, x, "x")
+        B, x_stride = (shape[0], strides[0]) if dim == 2 else (1, self.d_in)
+        out_stride = self.d_out
         if out is None:
-            if x.device != self.device:
-                raise ValueError(f"x is on {x.device}, not on {self.device}")
-            out = _empty((B, self.d_out) if dim == 2 else (self.d_out,), x.dtype, x.device, stream)
-            out_stride = self.d_out
+            out = _empty(x, (B, out_stride) if dim == 2 else (out_stride,), x.dtype, stream)
         else:
-            _same_device(self.device, x=x, out=out)
+            _on(index, out, "out")
             if out.dtype != x.dtype or out.dim() != dim or out.shape[-1] != self.d_out \
                     or out.stride(-1) != 1 or (dim == 2 and out.shape[0] != B):
                 raise ValueError(f"out must be {x.dtype} of {B} rows of {self.d_out} contiguous values")
-            out_stride = out.stride(0) if dim == 2 else self.d_out
-        check(lib.prox_linear4_forward(self.handle, x.data_ptr(), x.stride(0) if dim == 2 else self.d_in,
-                                       out.data_ptr(), out_stride, B, dt, _raw_stream(stream, x.device)))
+            if dim == 2:
+                out_stride = out.stride(0)
+        check(lib.prox_linear4_forward(self.handle, x.data_ptr(), x_stride, out.data_ptr(), out_stride, B, dt,
+                                       _raw_stream(stream, index)))
         return out
 
     __call__ = forward
@@ -172,6 +183,8 @@ class KVCache4:
         self.num_pages, self.n_heads, self.page_size = k_codes.shape[:3]
         self.head_dim = 2 * k_codes.shape[3]
         self.device = k_codes.device
+        self._index = self.device.index
+        self._scale = 1.0 / math.sqrt(self.head_dim)
         self.k_codes, self.k_scales, self.v_codes, self.v_scales = k_codes, k_scales, v_codes, v_scales
         h = ctypes.c_void_p(0)
         check(lib.prox_kv4_create(k_codes.data_ptr(), k_scales.data_ptr(), v_codes.data_ptr(),
@@ -209,24 +222,25 @@ class KVCache4:
     def error_word(self, stream=None) -> int:
         """DEVERR_SLOT / DEVERR_PAGE / DEVERR_LEN bits since the last call (synchronises)."""
         v = ctypes.c_int32(0)
-        check(lib.prox_kv4_error(self.handle, ctypes.byref(v), _raw_stream(stream, self.device)))
+        check(lib.prox_kv4_error(self.handle, ctypes.byref(v), _raw_stream(stream, self._index)))
         return int(v.value)
 
     def append(self, k: torch.Tensor, v: torch.Tensor, slots: torch.Tensor, stream=None) -> None:
         """Quantises rows k, v [T, heads, head_dim] (any strides, values
         contiguous) into slots (int64 [T]; negative: skipped)."""
         dt = _act(k, "k")
-        shape = k.shape
+        shape, ks, vs, index = k.shape, k.stride(), v.stride(), self._index
         if len(shape) != 3 or shape[1] != self.n_heads or shape[2] != self.head_dim or v.shape != shape \
-                or k.stride(2) != 1 or v.stride(2) != 1:
+                or ks[2] != 1 or vs[2] != 1:
             raise ValueError(f"k and v must be [T, {self.n_heads}, {self.head_dim}] with contiguous rows")
         if v.dtype != k.dtype:
             raise TypeError(f"k and v must have one type, got {k.dtype} and {v.dtype}")
         _ints(slots, torch.int64, shape[0], "slots")
-        _same_device(self.device, k=k, v=v, slots=slots)
-        check(lib.prox_kv4_append(self.handle, k.data_ptr(), v.data_ptr(), k.stride(0), k.stride(1),
-                                  v.stride(0), v.stride(1), slots.data_ptr(), shape[0], dt,
-                                  _raw_stream(stream, self.device)))
+        _on(index, k, "k")
+        _on(index, v, "v")
+        _on(index, slots, "slots")
+        check(lib.prox_kv4_append(self.handle, k.data_ptr(), v.data_ptr(), ks[0], ks[1], vs[0], vs[1],
+                                  slots.data_ptr(), shape[0], dt, _raw_stream(stream, index)))
 
     def read(self, slots: torch.Tensor, dtype: torch.dtype = torch.float32,
              stream=None) -> tuple[torch.Tensor, torch.Tensor]:
@@ -236,10 +250,11 @@ class KVCache4:
             raise TypeError(f"dtype must be float32, float16 or bfloat16, got {dtype}")
         T = slots.numel()
         _ints(slots, torch.int64, T, "slots")
-        _same_device(self.device, slots=slots)
-        k, v = _empty((2, T, self.n_heads, self.head_dim), dtype, self.device, stream).unbind(0)
+        _on(self._index, slots, "slots")
+        shape = (T, self.n_heads, self.head_dim)
+        k, v = _empty(slots, shape, dtype, stream), _empty(slots, shape, dtype, stream)
         check(lib.prox_kv4_read(self.handle, slots.data_ptr(), T, k.data_ptr(), v.data_ptr(), DTYPES[dtype],
-                                _raw_stream(stream, self.device)))
+                                _raw_stream(stream, self._index)))
         return k, v
 
     def attend(self, q: torch.Tensor, table: torch.Tensor, lens: torch.Tensor, scale: float | None = None,
@@ -249,30 +264,32 @@ class KVCache4:
         lens int32 [B], the cached tokens with the new ones among them.  scale
         defaults to head_dim ** -0.5.  lse: optional fp32 [B, Tq, Hq]."""
         dt = _act(q, "q")
-        dim = q.dim()
-        if dim not in (3, 4) or q.shape[-1] != self.head_dim or q.stride(-1) != 1:
+        shape, strides, index = q.shape, q.stride(), self._index
+        dim = len(shape)
+        if dim not in (3, 4) or shape[-1] != self.head_dim or strides[-1] != 1:
             raise ValueError(f"q must be [B, Tq, Hq, {self.head_dim}] or [B, Hq, {self.head_dim}] with "
-                             f"contiguous rows, got {tuple(q.shape)}")
-        B, Hq = q.shape[0], q.shape[-2]
-        Tq = q.shape[1] if dim == 4 else 1
-        if not isinstance(table, torch.Tensor) or table.dtype != torch.int32 or table.dim() != 2 \
-                or table.shape[0] != B or (table.shape[1] > 1 and table.stride(1) != 1):
-            raise ValueError(f"table must be int32 [{B}, cols] with contiguous rows")
+                             f"contiguous rows, got {tuple(shape)}")
+        B, Hq = shape[0], shape[-2]
+        Tq, q_tok = (shape[1], strides[1]) if dim == 4 else (1, 0)
+        cols, table_stride = _table(table, B)
         _ints(lens, torch.int32, B, "lens")
-        _same_device(self.device, q=q, table=table, lens=lens, out=out, lse=lse)
+        _on(index, q, "q")
+        _on(index, table, "table")
+        _on(index, lens, "lens")
         if out is None:
-            out = _empty(q.shape, q.dtype, self.device, stream)
-        elif out.dtype != q.dtype or out.shape != q.shape or not out.is_contiguous():
-            raise ValueError("out must be a contiguous tensor of q's shape and type")
-        if lse is not None and (lse.dtype != torch.float32 or lse.numel() != B * Tq * Hq
-                                or not lse.is_contiguous()):
-            raise ValueError(f"lse must hold {B * Tq * Hq} contiguous float32 values")
-        cols = table.shape[1]
-        check(lib.prox_kv4_attend(self.handle, q.data_ptr(), q.stride(0), q.stride(1) if dim == 4 else 0,
-                                  q.stride(-2), Hq, B, Tq, table.data_ptr(), max(table.stride(0), cols), cols,
-                                  lens.data_ptr(), 1.0 / math.sqrt(self.head_dim) if scale is None else scale,
-                                  out.data_ptr(), None if lse is None else lse.data_ptr(), dt,
-                                  _raw_stream(stream, self.device)))
+            out = _empty(q, shape, q.dtype, stream)
+        else:
+            _on(index, out, "out")
+            if out.dtype != q.dtype or out.shape != shape or not out.is_contiguous():
+                raise ValueError("out must be a contiguous tensor of q's shape and type")
+        if lse is not None:
+            _on(index, lse, "lse")
+            if lse.dtype != torch.float32 or lse.numel() != B * Tq * Hq or not lse.is_contiguous():
+                raise ValueError(f"lse must hold {B * Tq * Hq} contiguous float32 values")
+        check(lib.prox_kv4_attend(self.handle, q.data_ptr(), strides[0], q_tok, strides[-2], Hq, B, Tq,
+                                  table.data_ptr(), table_stride, cols, lens.data_ptr(),
+                                  self._scale if scale is None else scale, out.data_ptr(),
+                                  None if lse is None else lse.data_ptr(), dt, _raw_stream(stream, index)))
         return out
 
 
@@ -301,24 +318,22 @@ def plan_pages(lens: torch.Tensor, delta: torch.Tensor, table: torch.Tensor, fre
     _ints(lens, torch.int32, B, "lens")
     _ints(delta, torch.int32, B, "delta")
     _ints(free_count, torch.int32, 1, "free_count")
-    _ints(free_pages, torch.int32, free_pages.numel(), "free_pages")
-    if not isinstance(table, torch.Tensor) or table.dtype != torch.int32 or table.dim() != 2 \
-            or table.shape[0] != B or (table.shape[1] > 1 and table.stride(1) != 1):
-        raise ValueError(f"table must be int32 [{B}, cols] with contiguous rows")
+    cap = free_pages.numel()
+    _ints(free_pages, torch.int32, cap, "free_pages")
+    cols, table_stride = _table(table, B)
     if max_new < 0:
         raise ValueError(f"max_new={max_new} must be >= 0")
-    dev = lens.device
-    _same_device(dev, delta=delta, table=table, free_pages=free_pages, free_count=free_count)
+    index = lens.get_device()
+    for t, name in ((delta, "delta"), (table, "table"), (free_pages, "free_pages"), (free_count, "free_count")):
+        _on(index, t, name)
     Linear4._on_device(lens)
-    buf = _empty((2 * B + 3 + max_new,), torch.int32, dev, stream)
-    new_lens, cu, count, status, positions = buf.split_with_sizes([B, B + 1, 1, 1, max_new])
-    slots = _empty((max_new,), torch.int64, dev, stream)
+    buf = _empty(lens, (2 * B + 3 + max_new,), torch.int32, stream)
+    positions, new_lens, cu, count, status = buf.split_with_sizes([max_new, B, B + 1, 1, 1])
+    slots = _empty(lens, (max_new,), torch.int64, stream)
     if commit:
         new_lens, count = lens, free_count
-    cols = table.shape[1]
-    check(lib.prox_plan_pages(lens.data_ptr(), delta.data_ptr(), B, int(page_size), table.data_ptr(),
-                              max(table.stride(0), cols), cols, free_pages.data_ptr(), free_pages.numel(),
-                              free_count.data_ptr(), new_lens.data_ptr(), count.data_ptr(), cu.data_ptr(),
-                              slots.data_ptr(), positions.data_ptr(), max_new, status.data_ptr(),
-                              _raw_stream(stream, dev)))
+    check(lib.prox_plan_pages(lens.data_ptr(), delta.data_ptr(), B, int(page_size), table.data_ptr(), table_stride,
+                              cols, free_pages.data_ptr(), cap, free_count.data_ptr(), new_lens.data_ptr(),
+                              count.data_ptr(), cu.data_ptr(), slots.data_ptr(), positions.data_ptr(), max_new,
+                              status.data_ptr(), _raw_stream(stream, index)))
     return PagePlan(new_lens, count, cu, slots, positions, status)
