@@ -19,14 +19,14 @@ import torch
 from ._lib import (ACT_GELU_ERF, ACT_GELU_TANH, ACT_SILU, DEVERR_LEN, DEVERR_MASK_INDEX, DEVERR_PAGE,
                    DEVERR_SLOT, DEVERR_WAIT_TIMEOUT, MASK_THRESHOLD, MASK_TOPK, STAGE2_EXACT, STAGE2_PROXY_VALUES, LayerInfo,
                    ProxError, check, last_error, lib)
-from .decode4 import KVCache4, Linear4, PagePlan, plan_pages
+from .decode4 import Attention4, KVCache4, Linear4, PagePlan, plan_pages
 
 __all__ = ["Layer", "phase_times_us", "pack_proxy", "calibrate_thresholds", "rmsnorm", "copy", "version",
            "effective_sparsity", "allocate_sparsity", "runtime_sparsity", "ALPHA",
            "ACT_SILU", "ACT_GELU_TANH", "ACT_GELU_ERF", "STAGE2_EXACT", "STAGE2_PROXY_VALUES",
            "ProxError", "DEVERR_MASK_INDEX", "DEVERR_WAIT_TIMEOUT", "MASK_TOPK", "MASK_THRESHOLD",
            "DEVERR_SLOT", "DEVERR_PAGE", "DEVERR_LEN",
-           "Linear4", "KVCache4", "PagePlan", "plan_pages", "last_error", "lib"]
+           "Attention4", "Linear4", "KVCache4", "PagePlan", "plan_pages", "last_error", "lib"]
 
 GROUP = 128
 

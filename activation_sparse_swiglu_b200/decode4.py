@@ -337,3 +337,46 @@ def plan_pages(lens: torch.Tensor, delta: torch.Tensor, table: torch.Tensor, fre
                               count.data_ptr(), cu.data_ptr(), slots.data_ptr(), positions.data_ptr(), max_new,
                               status.data_ptr(), _raw_stream(stream, index)))
     return PagePlan(new_lens, count, cu, slots, positions, status)
+
+
+class Attention4:
+    """One attention sub-layer of a decoder block in 4 bits, for tokens of a
+    decode step: the query, key and value projections, the new rows into a
+    cache of its own, the attention over it and the output projection.
+
+    w_qkv: bf16 [d, (n_heads + 2 n_kv_heads) head_dim] (queries, then keys, then
+    values), w_o: bf16 [n_heads head_dim, d]; quantised by pack_proxy's rule.
+    rotate: optional callable (q, k, positions) -> (q, k) that applies the
+    model's position encoding to q [n, n_heads, head_dim] and k [n, n_kv_heads,
+    head_dim].  The cache has num_pages pages of page_size tokens; which rows a
+    step's tokens take is the caller's plan (plan_pages), shared by all layers.
+    """
+
+    def __init__(self, w_qkv: torch.Tensor, w_o: torch.Tensor, n_heads: int, n_kv_heads: int,
+                 head_dim: int, num_pages: int, page_size: int = 64, rotate=None, stream=None):
+        if n_heads < 1 or n_kv_heads < 1 or n_heads % n_kv_heads:
+            raise ValueError(f"n_heads={n_heads} must be a multiple of n_kv_heads={n_kv_heads}")
+        if w_qkv.dim() != 2 or w_qkv.shape[1] != (n_heads + 2 * n_kv_heads) * head_dim \
+                or tuple(w_o.shape) != (n_heads * head_dim, w_qkv.shape[0]):
+            raise ValueError("inconsistent weight shapes")
+        self.n_heads, self.n_kv_heads, self.head_dim = n_heads, n_kv_heads, head_dim
+        self.qkv, self.out = Linear4(w_qkv, stream=stream), Linear4(w_o, stream=stream)
+        self.cache = KVCache4.zeros(num_pages, n_kv_heads, page_size, head_dim, device=w_qkv.device)
+        self.rotate = rotate
+
+    def step(self, x: torch.Tensor, plan: PagePlan, table: torch.Tensor, stream=None) -> torch.Tensor:
+        """x [B, d], one new token of each request (B <= 16), under a plan in
+        which every request gains one -> [B, d]."""
+        B, D = x.shape[0], self.head_dim
+        heads = self.qkv.forward(x, stream=stream).view(B, self.n_heads + 2 * self.n_kv_heads, D)
+        q, k, v = heads.split_with_sizes([self.n_heads, self.n_kv_heads, self.n_kv_heads], 1)
+        if self.rotate is not None:
+            q, k = self.rotate(q, k, plan.positions[:B])
+        self.cache.append(k, v, plan.slots[:B], stream=stream)
+        o = self.cache.attend(q, table, plan.lens, stream=stream)
+        return self.out.forward(o.view(B, self.n_heads * D), stream=stream)
+
+    def close(self):
+        self.qkv.close()
+        self.out.close()
+        self.cache.close()

@@ -62,10 +62,14 @@ def thresholds_from_json(text: str) -> dict:
 
 
 class Stack:
-    def __init__(self, weights, k: int, max_batch: int = 1, stream=None):
+    def __init__(self, weights, k: int, max_batch: int = 1, stream=None, attention=None):
         """weights: sequence of (w_gate, w_up, w_down) bf16 CUDA tensors, math
         layout ([d, F], [d, F], [F, d]).  Thresholds start at 0 until
-        calibrate() sets them."""
+        calibrate() sets them.  attention: optional sequence of one attention
+        sub-layer (Attention4) per layer, which decode() runs before it."""
+        if attention is not None and len(attention) != len(weights):
+            raise ValueError(f"{len(attention)} attention sub-layers for {len(weights)} layers")
+        self.attention = None if attention is None else list(attention)
         self.layers = [Layer(wg, wu, wd, tau=0.0, k=k, max_batch=max_batch, stream=stream)
                        for (wg, wu, wd) in weights]
         self.taus = [0.0] * len(self.layers)
@@ -141,7 +145,26 @@ class Stack:
                 x = rmsnorm(y, stream=stream)
         return xs, y
 
+    def decode(self, x: torch.Tensor, plan, table: torch.Tensor, stream=None) -> torch.Tensor:
+        """One decode step of B requests through attention and FFN of every
+        layer, each chained to the next through unit-gain RMSNorm: x [B, d] the
+        requests' new tokens, plan the plan_pages() result in which every
+        request gains one token, table its page table.  Returns the last
+        layer's output [B, d]."""
+        if self.attention is None:
+            raise RuntimeError("the stack has no attention sub-layers")
+        y = None
+        for li, (attn, layer) in enumerate(zip(self.attention, self.layers)):
+            if li > 0:
+                x = rmsnorm(y, stream=stream)
+            a = attn.step(x, plan, table, stream=stream)
+            y = layer.forward(rmsnorm(a, stream=stream), stream=stream)
+        return y
+
     def close(self):
+        for attn in self.attention or []:
+            attn.close()
+        self.attention = None
         for layer in self.layers:
             layer.close()
         self.layers = []

@@ -644,3 +644,81 @@ def test_decode_steps_of_a_small_model(prox):
     pages = [p for b in range(B) for p in table[b, :-(-int(lens[b]) // page)].tolist()] + free[:40 - live].tolist()
     assert sorted(pages) == list(range(40))
     assert cache.error_word() == 0
+
+
+def test_stack_decodes_through_attention(prox):
+    """Stack.decode: three steps of four requests through two layers, each stage
+    against the plain forms fed with the library's own input to it, and equal to
+    the same calls made one by one."""
+    from activation_sparse_swiglu_b200.stack import Stack
+    from oracle import prox_oracle as orc
+    d, F, Hq, Hkv, D, B, n_layers, page = 256, 512, 4, 2, 64, 4, 2, 16
+    g = gen_of(30)
+    w = lambda *s: (0.05 * torch.randn(s, device="cuda", generator=g)).to(torch.bfloat16)  # noqa: E731
+    ffn = [(w(d, F), w(d, F), w(F, d)) for _ in range(n_layers)]
+    qkv, wo = [w(d, (Hq + 2 * Hkv) * D) for _ in range(n_layers)], [w(Hq * D, d) for _ in range(n_layers)]
+    seen = []
+
+    def rotate(q, k, positions):
+        seen.append(positions.tolist())
+        turn = 1.0 - 0.01 * positions.to(q.dtype)[:, None, None]
+        return q * turn, k * turn
+
+    def build():
+        attn = [prox.Attention4(a, o, Hq, Hkv, D, num_pages=12, page_size=page, rotate=rotate)
+                for a, o in zip(qkv, wo)]
+        return Stack(ffn, k=F, max_batch=B, attention=attn)
+
+    stack, by_hand = build(), build()
+    lens = torch.tensor([0, 15, 31, 2], dtype=torch.int32, device="cuda")
+    old = lens.clone()
+    table = torch.tensor([[-1, -1, -1], [7, -1, -1], [3, 5, -1], [1, -1, -1]], dtype=torch.int32, device="cuda")
+    free, count = (torch.tensor(x, dtype=torch.int32, device="cuda") for x in ([0, 2, 4, 6, 8, 9, 10, 11], [8]))
+    for a, b in zip(stack.attention, by_hand.attention):  # earlier tokens: the same rows in both
+        s = torch.cat([table[i, torch.arange(int(n)) // page].long() * page + torch.arange(int(n), device="cuda") % page
+                       for i, n in enumerate(old.tolist()) if n])
+        k, v = (torch.randn((s.numel(), Hkv, D), device="cuda", generator=g) for _ in range(2))
+        a.cache.append(k, v, s)
+        b.cache.append(k, v, s)
+    one = torch.ones(B, dtype=torch.int32, device="cuda")
+    for step in range(3):
+        plan = prox.plan_pages(lens, one, table, free, count, page, max_new=B, commit=True)
+        assert int(plan.status) == 0 and plan.positions.tolist() == (old + step).tolist()
+        x = torch.randn((B, d), device="cuda", generator=g)
+        y = stack.decode(x, plan, table)
+        h = x
+        for li in range(n_layers):
+            at = by_hand.attention[li]
+            want, tol = ref.linear4(h, *prox.pack_proxy(qkv[li]))
+            proj = at.qkv(h)
+            within(proj, want, tol)
+            heads = proj.view(B, Hq + 2 * Hkv, D)
+            q, k = rotate(heads[:, :Hq], heads[:, Hq:Hq + Hkv], plan.positions[:B])
+            at.cache.append(k, heads[:, Hq + Hkv:], plan.slots[:B])
+            o = at.cache.attend(q, table, plan.lens)
+            want, _, tol, _ = ref.attend(q[:, None], at.cache.k_codes, at.cache.k_scales, at.cache.v_codes,
+                                         at.cache.v_scales, table, plan.lens, D ** -0.5)
+            within(o[:, None], want, tol)
+            a = at.out(o.view(B, Hq * D))
+            z = prox.rmsnorm(a)
+            out = by_hand.layers[li].forward(z)
+            for b in range(B):  # k = d_ff and tau 0: the dense FFN
+                dense = orc.dense_ffn(z[b].cpu().numpy(), *(t.float().cpu().numpy() for t in ffn[li]))
+                got = out[b].double().cpu()
+                assert float((got - torch.from_numpy(dense)).norm()) <= 5e-3 * float(torch.from_numpy(dense).norm())
+            h = prox.rmsnorm(out)
+        assert torch.equal(y, out)
+    for a, b in zip(stack.attention, by_hand.attention):
+        for name in ("k_codes", "k_scales", "v_codes", "v_scales"):
+            assert torch.equal(getattr(a.cache, name), getattr(b.cache, name))
+        assert a.cache.error_word() == 0
+    stack.close()
+    by_hand.close()
+    with pytest.raises(RuntimeError):
+        Stack(ffn, k=F).decode(x, plan, table)
+    with pytest.raises(ValueError):
+        Stack(ffn, k=F, attention=[None])
+    with pytest.raises(ValueError):
+        prox.Attention4(qkv[0], wo[0], 4, 3, D, num_pages=4)
+    with pytest.raises(ValueError):
+        prox.Attention4(qkv[0], qkv[0], Hq, Hkv, D, num_pages=4)
