@@ -67,8 +67,9 @@ constexpr int kSmemLimit = 227 * 1024 - 2048;  // dynamic, beside the joins' tab
 // Cache rows of a step, and steps in flight or in use per warp.
 constexpr int step_rows(int D) { return D == 256 ? 32 : 64; }
 // Warps: as many as the registers of the column tiles allow.
-constexpr int warps_of(int D, int nt) { return D == 256 || nt == 2 ? 8 : kMaxWarps; }
-constexpr int stages_of(int D, int nt) { return warps_of(D, nt) == 8 ? 3 : 2; }
+constexpr int warps_of(int D, int nt, int parts) { return D == 256 || (nt == 2 && parts == 1) ? 8 : kMaxWarps; }
+constexpr int stages_of(int D, int nt, int parts) { return warps_of(D, nt, parts) == 8 ? 3 : 2; }
+constexpr int parts_of(int dtype) { return dtype == PROX_F32 ? 2 : 1; }
 
 struct AttendArgs {
   Attend4Call c;
@@ -134,9 +135,9 @@ struct Chain {
 };
 
 template <int DT, int D, int NT>
-__global__ void __launch_bounds__(warps_of(D, NT) * 32, 1) attend4_kernel(const AttendArgs a) {
+__global__ void __launch_bounds__(warps_of(D, NT, parts_of(DT)) * 32, 1) attend4_kernel(const AttendArgs a) {
   using T = typename Act<DT>::T;
-  constexpr int PARTS = DT == PROX_F32 ? 2 : 1;
+  constexpr int PARTS = parts_of(DT);
   constexpr bool EXACT = PARTS == 2;   // codes as exact integers, not offset subnormals
   constexpr int RB = 8 * NT / PARTS;   // rows of a block
   constexpr int NC = 2 / PARTS;        // rows a thread has per column tile
@@ -145,7 +146,7 @@ __global__ void __launch_bounds__(warps_of(D, NT) * 32, 1) attend4_kernel(const 
   constexpr int PIECES = D / 32;       // 16-byte pieces of a row
   constexpr int ROWS = step_rows(D);
   constexpr int MT = ROWS / 16;        // tiles of 16 tokens
-  constexpr int STAGES = stages_of(D, NT);
+  constexpr int STAGES = stages_of(D, NT, PARTS);
   constexpr int SB = stage_bytes<D>();
   constexpr int SLOT = part_floats(RB, D);
   static_assert(SLOT * 4 <= STAGES * SB, "a part fits a ring");
@@ -221,15 +222,28 @@ __global__ void __launch_bounds__(warps_of(D, NT) * 32, 1) attend4_kernel(const 
     s.beg = (long long)H * (pre[lo] - kStartUnits * lo) + (long long)hb * s.n;
     return s;
   };
-  auto unit_at = [&](long long place) {
-    if (place >= places) return (long long)H * (total - (long long)kStartUnits * c.B);
-    const Cursor s = seek(place);
-    return s.beg + s.c;
-  };
+  // Three places sought at once, in three lanes: the CTA's first, the warp's
+  // first and the one behind its last.
   const long long cta0 = places * blockIdx.x / P, cta1 = places * (blockIdx.x + 1) / P;
-  const long long cb = unit_at(cta0);
-  Cursor start = seek(cta0 + (cta1 - cta0) * warp / warps);
-  const long long wb = start.beg + start.c, we = unit_at(cta0 + (cta1 - cta0) * (warp + 1) / warps);
+  Cursor start;
+  long long cb, wb, we;
+  {
+    const long long all = (long long)H * (total - (long long)kStartUnits * c.B);  // units
+    const unsigned span = (unsigned)(cta1 - cta0);  // (H 2^27 / P at most, times 12)
+    const long long place = lane == 0 ? cta0 : cta0 + (long long)span * (warp + (lane == 2)) / warps;
+    Cursor s = seek(place < places ? place : places - 1);
+    const long long u = place < places ? s.beg + s.c : all;
+    cb = __shfl_sync(0xffffffffu, u, 0);
+    wb = __shfl_sync(0xffffffffu, u, 1);
+    we = __shfl_sync(0xffffffffu, u, 2);
+    start.b = __shfl_sync(0xffffffffu, s.b, 1);
+    start.head = __shfl_sync(0xffffffffu, s.head, 1);
+    start.block = __shfl_sync(0xffffffffu, s.block, 1);
+    start.c = __shfl_sync(0xffffffffu, s.c, 1);
+    start.n = __shfl_sync(0xffffffffu, s.n, 1);
+    start.len = __shfl_sync(0xffffffffu, s.len, 1);
+    start.beg = __shfl_sync(0xffffffffu, s.beg, 1);
+  }
 
   // n units on, to the next context at its end (not past the last unit)
   auto advance = [&](Cursor& s, int n) {
@@ -769,6 +783,26 @@ __global__ void __launch_bounds__(warps_of(D, NT) * 32, 1) attend4_kernel(const 
     store_vals<DT, 4>(static_cast<T*>(c.out) + o + d, true, y);
     if (c.lse && d == 0) c.lse[o / D] = l == 0.f ? -INFINITY : 0.6931471805599453f * (top + log2f(l));
   };
+  // adds parts with maxima m (-inf: none), sums q and values o to top, l and y
+  auto add_parts = [](const auto& m, const auto& q, const auto& o, float* top, float* l, float(&y)[4]) {
+    constexpr int n = sizeof(m) / sizeof(m[0]);
+    float up = *top;
+#pragma unroll
+    for (int i = 0; i < n; ++i) up = fmaxf(up, m[i]);
+    const float base = up == -INFINITY ? 0.f : up;
+    float f = exp2_fast(*top - base);
+    *top = up;
+    *l *= f;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) y[i] *= f;
+#pragma unroll
+    for (int i = 0; i < n; ++i) {
+      f = exp2_fast(m[i] - base);  // 0 without a visible row (a NaN in the part stays)
+      *l = fmaf(q[i], f, *l);
+      y[0] = fmaf(o[i].x, f, y[0]), y[1] = fmaf(o[i].y, f, y[1]);
+      y[2] = fmaf(o[i].z, f, y[2]), y[3] = fmaf(o[i].w, f, y[3]);
+    }
+  };
   for (int e = threadIdx.x; e < chains * kSlices; e += blockDim.x) {
     const Chain& ch = s_chain[e / kSlices];
     const int row = e % kSlices / (D / 4), d = e % (D / 4) * 4;
@@ -790,20 +824,7 @@ __global__ void __launch_bounds__(warps_of(D, NT) * 32, 1) attend4_kernel(const 
         q[i] = p[i] ? p[i][RB * D + RB + row] : 0.f;
         o[i] = p[i] ? *reinterpret_cast<const float4*>(p[i] + row * D + d) : make_float4(0.f, 0.f, 0.f, 0.f);
       }
-      const float up = fmaxf(fmaxf(fmaxf(m[0], m[1]), fmaxf(m[2], m[3])), top);
-      const float base = up == -INFINITY ? 0.f : up;
-      float f = exp2_fast(top - base);
-      top = up;
-      l *= f;
-#pragma unroll
-      for (int i = 0; i < 4; ++i) y[i] *= f;
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        f = exp2_fast(m[i] - base);  // 0 where there is no part
-        l = fmaf(q[i], f, l);
-        y[0] = fmaf(o[i].x, f, y[0]), y[1] = fmaf(o[i].y, f, y[1]);
-        y[2] = fmaf(o[i].z, f, y[2]), y[3] = fmaf(o[i].w, f, y[3]);
-      }
+      add_parts(m, q, o, &top, &l, y);
     }
     const bool left = ch.s.beg < cb;  // began in an earlier CTA
     result(ch.s, row, d, top, l, y,
@@ -848,19 +869,19 @@ __global__ void __launch_bounds__(warps_of(D, NT) * 32, 1) attend4_kernel(const 
     auto part = [&](int cta) { return a.part + (size_t)(2 * cta + (cta == c0 ? 1 : 0)) * SLOT; };
     for (int e = threadIdx.x; e < kSlices; e += blockDim.x) {
       const int row = e / (D / 4), d = e % (D / 4) * 4;
-      float top = -INFINITY;
-#pragma unroll 8
-      for (int i = c0; i <= c1; ++i) top = fmaxf(top, __ldcg(part(i) + RB * D + row));
-      const float base = top == -INFINITY ? 0.f : top;
-      float l = 0.f, y[4] = {};
-#pragma unroll 4
-      for (int i = c0; i <= c1; ++i) {
-        const float* p = part(i);
-        const float f = exp2_fast(__ldcg(p + RB * D + row) - base);
-        const float4 o = __ldcg(reinterpret_cast<const float4*>(p + row * D + d));
-        l = fmaf(__ldcg(p + RB * D + RB + row), f, l);
-        y[0] = fmaf(o.x, f, y[0]), y[1] = fmaf(o.y, f, y[1]);
-        y[2] = fmaf(o.z, f, y[2]), y[3] = fmaf(o.w, f, y[3]);
+      float top = -INFINITY, l = 0.f, y[4] = {};
+      for (int i0 = c0; i0 <= c1; i0 += 8) {
+        float m[8], q[8];
+        float4 o[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const bool there = i0 + i <= c1;
+          const float* p = part(there ? i0 + i : c1);
+          m[i] = there ? __ldcg(p + RB * D + row) : -INFINITY;
+          q[i] = __ldcg(p + RB * D + RB + row);
+          o[i] = __ldcg(reinterpret_cast<const float4*>(p + row * D + d));
+        }
+        add_parts(m, q, o, &top, &l, y);
       }
       result(s, row, d, top, l, y, nullptr);
     }
@@ -885,13 +906,13 @@ Kernel pick(int dtype, int D, int nt) {
 // Two column tiles where one does not hold a kv head's rows; head_dim 256
 // would not fit the registers with two.
 int col_tiles(int R, int dtype, int D) {
-  const int rb = dtype == PROX_F32 ? 4 : 8;
+  const int rb = 8 / parts_of(dtype);
   return R <= rb || D == 256 ? 1 : 2;
 }
 
-size_t smem_bytes(int warps, int D, int nt, int B) {
+size_t smem_bytes(int warps, int D, int nt, int dtype, int B) {
   const size_t rows = step_rows(D);
-  return (size_t)warps * (stages_of(D, nt) * rows * (D + 4) + rows * 8) + (size_t)(B + 1) * 4;
+  return (size_t)warps * (stages_of(D, nt, parts_of(dtype)) * rows * (D + 4) + rows * 8) + (size_t)(B + 1) * 4;
 }
 
 }  // namespace
@@ -921,7 +942,7 @@ cudaError_t launch_attend4(const prox_kv4* C, const Attend4Call& c, cudaStream_t
   a.G = c.Hq / C->heads;
   a.R = a.G * c.Tq;
   const int nt = col_tiles(a.R, c.dtype, C->D);
-  const int rb = 8 * nt / (c.dtype == PROX_F32 ? 2 : 1);
+  const int rb = 8 * nt / parts_of(c.dtype);
   a.blocks = (a.R + rb - 1) / rb;
   a.err = C->err;
   a.part = C->part;
@@ -930,12 +951,12 @@ cudaError_t launch_attend4(const prox_kv4* C, const Attend4Call& c, cudaStream_t
   const int per16 = c.dtype == PROX_F32 ? 4 : 8;
   a.q_vec = (reinterpret_cast<uintptr_t>(c.q) & 15) == 0 && c.q_req % per16 == 0 && c.q_tok % per16 == 0 &&
             c.q_head % per16 == 0;
-  int warps = warps_of(C->D, nt);
-  while (smem_bytes(warps, C->D, nt, c.B) > (size_t)kSmemLimit) --warps;  // (large batches)
+  int warps = warps_of(C->D, nt, parts_of(c.dtype));
+  while (smem_bytes(warps, C->D, nt, c.dtype, c.B) > (size_t)kSmemLimit) --warps;  // (large batches)
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)C->num_sms, 1, 1);
   cfg.blockDim = dim3(warps * 32, 1, 1);
-  cfg.dynamicSmemBytes = smem_bytes(warps, C->D, nt, c.B);
+  cfg.dynamicSmemBytes = smem_bytes(warps, C->D, nt, c.dtype, c.B);
   cfg.stream = s;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
