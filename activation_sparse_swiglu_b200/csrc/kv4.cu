@@ -63,40 +63,18 @@ __device__ uint32_t code8_any(const float (&x)[8], float s) {
   return w;
 }
 
+// One row quantised into slot row `at` of codes and scales, by its LPR lanes.
 template <int DT, int D>
-__global__ void __launch_bounds__(kThreads) append_kernel(prox_kv4 C, const void* k_in, const void* v_in,
-                                                          int64_t k_token, int64_t k_head, int64_t v_token,
-                                                          int64_t v_head, const int64_t* slots, int T, int shift, bool vec) {
-  using T_ = typename Act<DT>::T;
-  constexpr int LPR = D / 16;  // lanes of one row
-  pdl_wait();
-  pdl_trigger();
-  const int lane = threadIdx.x % LPR;
-  const unsigned row = (unsigned)(((int64_t)blockIdx.x * kThreads + threadIdx.x) / LPR);
-  const bool is_v = blockIdx.y;
-  const unsigned t = row / (unsigned)C.heads, h = row - t * C.heads;
-  if (t >= (unsigned)T) return;  // a whole row's lanes leave together
-  const int64_t slot = slots[t];
-  if (slot < 0) return;
-  if (slot >= (int64_t)C.pages * C.page) {
-    if (lane == 0) atomicOr(C.err, PROX_DEVERR_SLOT);
-    return;
-  }
-  const T_* x = static_cast<const T_*>(is_v ? v_in : k_in) + (int64_t)t * (is_v ? v_token : k_token) +
-                (int64_t)h * (is_v ? v_head : k_head);
-  float a[8], b[8];
-  load_vals<DT, 8>(x + 8 * lane, vec, a);
-  load_vals<DT, 8>(x + D / 2 + 8 * lane, vec, b);
+__device__ __forceinline__ void put_row(const float (&a)[8], const float (&b)[8], int lane, unsigned mask,
+                                        uint8_t* codes, uint16_t* scales, int64_t at) {
+  constexpr int LPR = D / 16;
   float mx = 0.f;
 #pragma unroll
   for (int i = 0; i < 8; ++i) mx = max_nan(mx, max_nan(fabsf(a[i]), fabsf(b[i])));
-  const unsigned mask = (LPR == 32 ? 0xffffffffu : ((1u << LPR) - 1)) << ((threadIdx.x & 31) / LPR * LPR);
 #pragma unroll
   for (int o = LPR / 2; o > 0; o >>= 1) mx = max_nan(mx, __shfl_xor_sync(mask, mx, o));
   const __half sh = __float2half_rn(mx / 7.0f);
   const float s = __half2float(sh);
-  const int64_t at = (((slot >> shift) * C.heads + h) << shift) + (slot & (C.page - 1));
-  uint8_t* dst = (is_v ? C.v : C.k) + at * (D / 2);
   uint32_t ca, cb;
   if (s >= 0x1p-14f && s <= 65504.f) {
     const float rs = 1.0f / s, half = 0.5f * s;
@@ -106,9 +84,43 @@ __global__ void __launch_bounds__(kThreads) append_kernel(prox_kv4 C, const void
     ca = code8_any(a, s);
     cb = code8_any(b, s);
   }
-  *reinterpret_cast<uint32_t*>(dst + 4 * lane) = ca;
-  *reinterpret_cast<uint32_t*>(dst + D / 4 + 4 * lane) = cb;
-  if (lane == 0) reinterpret_cast<__half*>(is_v ? C.vs : C.ks)[at] = sh;
+  uint8_t* dst = codes + at * (D / 2) + 4 * lane;
+  *reinterpret_cast<uint32_t*>(dst) = ca;
+  *reinterpret_cast<uint32_t*>(dst + D / 4) = cb;
+  if (lane == 0) reinterpret_cast<__half*>(scales)[at] = sh;
+}
+
+// Each group of lanes takes a row of K and the same of V: one slot, one place.
+template <int DT, int D>
+__global__ void __launch_bounds__(kThreads) append_kernel(prox_kv4 C, const void* k_in, const void* v_in,
+                                                          int64_t k_token, int64_t k_head, int64_t v_token,
+                                                          int64_t v_head, const int64_t* slots, int T, int shift,
+                                                          bool vec) {
+  using T_ = typename Act<DT>::T;
+  constexpr int LPR = D / 16;  // lanes of one row
+  pdl_wait();
+  pdl_trigger();
+  const int lane = threadIdx.x % LPR;
+  const unsigned row = (unsigned)(((int64_t)blockIdx.x * kThreads + threadIdx.x) / LPR);
+  const unsigned t = row / (unsigned)C.heads, h = row - t * C.heads;
+  if (t >= (unsigned)T) return;  // a whole row's lanes leave together
+  const int64_t slot = slots[t];
+  const T_* k = static_cast<const T_*>(k_in) + (int64_t)t * k_token + (int64_t)h * k_head + 8 * lane;
+  const T_* v = static_cast<const T_*>(v_in) + (int64_t)t * v_token + (int64_t)h * v_head + 8 * lane;
+  float ka[8], kb[8], va[8], vb[8];
+  if (slot < 0) return;
+  if (slot >= (int64_t)C.pages * C.page) {
+    if (lane == 0) atomicOr(C.err, PROX_DEVERR_SLOT);
+    return;
+  }
+  load_vals<DT, 8>(k, vec, ka);
+  load_vals<DT, 8>(k + D / 2, vec, kb);
+  load_vals<DT, 8>(v, vec, va);
+  load_vals<DT, 8>(v + D / 2, vec, vb);
+  const unsigned mask = ((1u << LPR) - 1) << ((threadIdx.x & 31) / LPR * LPR);
+  const int64_t at = (((slot >> shift) * C.heads + h) << shift) + (slot & (C.page - 1));
+  put_row<DT, D>(ka, kb, lane, mask, C.k, C.ks, at);
+  put_row<DT, D>(va, vb, lane, mask, C.v, C.vs, at);
 }
 
 // The eight values of a word under scale s, rounded once and stored.  (A code
@@ -144,25 +156,31 @@ __global__ void __launch_bounds__(kThreads) read_kernel(prox_kv4 C, const int64_
   pdl_wait();
   pdl_trigger();
   const int lane = threadIdx.x % LPR;
-  const int64_t row = ((int64_t)blockIdx.x * kThreads + threadIdx.x) / LPR;
-  const bool is_v = blockIdx.y;
-  if (row / C.heads >= T) return;
-  const int t = (int)(row / C.heads), h = (int)(row % C.heads);
+  const unsigned row = (unsigned)(((int64_t)blockIdx.x * kThreads + threadIdx.x) / LPR);
+  const unsigned t = row / (unsigned)C.heads, h = row - t * C.heads;
+  if (t >= (unsigned)T) return;
   const int64_t slot = slots[t];
-  T_* y = static_cast<T_*>(is_v ? v_out : k_out) + (int64_t)row * D;
-  uint32_t wa = 0x88888888u, wb = wa;
-  __half sc = __half(0.f);
+  uint32_t w[4] = {0x88888888u, 0x88888888u, 0x88888888u, 0x88888888u};
+  __half ks = __half(0.f), vs = __half(0.f);
   if (slot >= (int64_t)C.pages * C.page) {
     if (lane == 0) atomicOr(C.err, PROX_DEVERR_SLOT);
   } else if (slot >= 0) {
     const int64_t at = (((slot >> shift) * C.heads + h) << shift) + (slot & (C.page - 1));
-    const uint8_t* src = (is_v ? C.v : C.k) + at * (D / 2);
-    sc = reinterpret_cast<const __half*>(is_v ? C.vs : C.ks)[at];
-    wa = *reinterpret_cast<const uint32_t*>(src + 4 * lane);
-    wb = *reinterpret_cast<const uint32_t*>(src + D / 4 + 4 * lane);
+    const uint8_t* k = C.k + at * (D / 2) + 4 * lane;
+    const uint8_t* v = C.v + at * (D / 2) + 4 * lane;
+    ks = reinterpret_cast<const __half*>(C.ks)[at];
+    vs = reinterpret_cast<const __half*>(C.vs)[at];
+    w[0] = *reinterpret_cast<const uint32_t*>(k);
+    w[1] = *reinterpret_cast<const uint32_t*>(k + D / 4);
+    w[2] = *reinterpret_cast<const uint32_t*>(v);
+    w[3] = *reinterpret_cast<const uint32_t*>(v + D / 4);
   }
-  store8<DT>(y + 8 * lane, wa, sc);
-  store8<DT>(y + D / 2 + 8 * lane, wb, sc);
+  T_* ko = static_cast<T_*>(k_out) + (int64_t)row * D + 8 * lane;
+  T_* vo = static_cast<T_*>(v_out) + (int64_t)row * D + 8 * lane;
+  store8<DT>(ko, w[0], ks);
+  store8<DT>(ko + D / 2, w[1], ks);
+  store8<DT>(vo, w[2], vs);
+  store8<DT>(vo + D / 2, w[3], vs);
 }
 
 int shift_of(int page) {
@@ -173,7 +191,7 @@ int shift_of(int page) {
 
 cudaLaunchConfig_t rows_config(int64_t rows, int lanes, cudaStream_t s, cudaLaunchAttribute* attr) {
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)((rows * lanes + kThreads - 1) / kThreads), 2, 1);
+  cfg.gridDim = dim3((unsigned)((rows * lanes + kThreads - 1) / kThreads), 1, 1);
   cfg.blockDim = dim3(kThreads, 1, 1);
   cfg.stream = s;
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
