@@ -252,7 +252,8 @@ class KVCache4:
         _ints(slots, torch.int64, T, "slots")
         _on(self._index, slots, "slots")
         shape = (T, self.n_heads, self.head_dim)
-        k, v = _empty(slots, shape, dtype, stream), _empty(slots, shape, dtype, stream)
+        k = _empty(slots, shape, dtype, stream)
+        v = torch.empty_like(k) if stream is None else _empty(slots, shape, dtype, stream)
         check(lib.prox_kv4_read(self.handle, slots.data_ptr(), T, k.data_ptr(), v.data_ptr(), DTYPES[dtype],
                                 _raw_stream(stream, self._index)))
         return k, v
@@ -277,7 +278,7 @@ class KVCache4:
         _on(index, table, "table")
         _on(index, lens, "lens")
         if out is None:
-            out = _empty(q, shape, q.dtype, stream)
+            out = torch.empty_like(q) if stream is None and q.is_contiguous() else _empty(q, shape, q.dtype, stream)
         else:
             _on(index, out, "out")
             if out.dtype != q.dtype or out.shape != shape or not out.is_contiguous():
