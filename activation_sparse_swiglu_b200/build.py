@@ -1,4 +1,5 @@
-"""Builds libprox.so (all CUDA sources, sm_100a) next to this file.
+"""Builds libprox.so (all CUDA sources, sm_100a) and the Python entry of the
+4-bit operators (_decode4.so) next to this file.
 
 Usage: python activation_sparse_swiglu_b200/build.py [--force] [--verbose] [--ptxas-info]
 (run by path: importing the package loads libprox.so, which may be missing or stale)
@@ -17,6 +18,8 @@ ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(PKG, "libprox.so")
+ENTRY = os.path.join(PKG, "_decode4.so")
+ENTRY_SOURCE = os.path.join(CSRC, "decode4_py.cpp")
 
 SOURCES = ["prox_api.cu", "token.cu", "batch.cu", "pack.cu", "calibrate.cu", "misc.cu",
            "decode4_api.cu", "linear4.cu", "kv4.cu", "attend4.cu", "pages.cu"]
@@ -54,6 +57,7 @@ def up_to_date() -> bool:
 
 def build(force: bool = False, verbose: bool = False, ptxas_info: bool = False) -> str:
     if not force and not ptxas_info and up_to_date():
+        build_entry()
         return LIB
     nvcc = _nvcc()
     tmp = LIB + ".tmp"
@@ -69,7 +73,34 @@ def build(force: bool = False, verbose: bool = False, ptxas_info: bool = False) 
     if ptxas_info or verbose:
         sys.stderr.write(proc.stderr)
     os.replace(tmp, LIB)
+    build_entry(force=force, verbose=verbose)
     return LIB
+
+
+def build_entry(force: bool = False, verbose: bool = False) -> str:
+    """_decode4.so: a CPython module over torch's tensors and libprox.so."""
+    inputs = [ENTRY_SOURCE, os.path.join(INCLUDE, "prox.h"), os.path.abspath(__file__)]
+    if not force and os.path.exists(ENTRY) and all(
+            os.path.getmtime(f) <= os.path.getmtime(ENTRY) for f in inputs):
+        return ENTRY
+    import importlib.util
+    import sysconfig
+    torch_dir = os.path.dirname(importlib.util.find_spec("torch").origin)
+    cuda = os.path.dirname(os.path.dirname(os.path.realpath(_nvcc())))
+    tmp = ENTRY + ".tmp"
+    cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden", "-o", tmp, ENTRY_SOURCE,
+           "-I", INCLUDE, "-isystem", os.path.join(torch_dir, "include"),
+           "-isystem", os.path.join(torch_dir, "include", "torch", "csrc", "api", "include"),
+           "-isystem", sysconfig.get_paths()["include"], "-isystem", os.path.join(cuda, "include"),
+           "-L", PKG, "-l:libprox.so", "-L", os.path.join(torch_dir, "lib"), "-ltorch_python", "-ltorch_cpu",
+           "-lc10", "-lc10_cuda", "-Wl,-rpath,$ORIGIN"]
+    if verbose:
+        print(" ".join(cmd), file=sys.stderr)
+    proc = subprocess.run(cmd, capture_output=True, text=True)
+    if proc.returncode != 0:
+        raise RuntimeError(f"g++ failed ({proc.returncode}):\n{proc.stdout}\n{proc.stderr}")
+    os.replace(tmp, ENTRY)
+    return ENTRY
 
 
 if __name__ == "__main__":

@@ -7,7 +7,8 @@ plan of the pages and slots that a step's tokens take.
     cache.append(k, v, plan.slots)
     o = cache.attend(q, table, plan.lens)              # [B, Hq, D]
 
-Argument checks and marshalling only; the arithmetic runs in libprox.so.
+Argument checks and marshalling only, most of it in the native module _decode4
+(csrc/decode4_py.cpp); the arithmetic runs in libprox.so.
 """
 
 from __future__ import annotations
@@ -18,9 +19,13 @@ from typing import NamedTuple
 
 import torch
 
-from ._lib import DTYPE_BF16, DTYPE_F16, DTYPE_F32, check, lib
+from ._lib import PKG, check, lib
 
-DTYPES = {torch.float32: DTYPE_F32, torch.float16: DTYPE_F16, torch.bfloat16: DTYPE_BF16}
+try:
+    from . import _decode4
+except ImportError as e:
+    raise ImportError(f"{PKG}/_decode4.so cannot be loaded: build it with `python {PKG}/build.py` "
+                      "(it is required; there is no fallback)") from e
 
 
 def _raw_stream(stream, index: int) -> int:
@@ -29,44 +34,12 @@ def _raw_stream(stream, index: int) -> int:
     return stream.cuda_stream if isinstance(stream, torch.cuda.Stream) else int(stream)
 
 
-def _empty(like: torch.Tensor, shape, dtype, stream) -> torch.Tensor:
-    """A result tensor on like's device that belongs to the stream that writes it."""
-    if stream is not None and isinstance(stream, torch.cuda.Stream):
+def _empty(device: torch.device, shape, dtype, stream) -> torch.Tensor:
+    """A result tensor that belongs to the stream that writes it."""
+    if isinstance(stream, torch.cuda.Stream):
         with torch.cuda.stream(stream):
-            return like.new_empty(shape, dtype=dtype)
-    return like.new_empty(shape, dtype=dtype)
-
-
-def _act(t: torch.Tensor, name: str) -> int:
-    """The library's code of t's type."""
-    code = DTYPES.get(t.dtype) if isinstance(t, torch.Tensor) and t.is_cuda else None
-    if code is not None:
-        return code
-    if not isinstance(t, torch.Tensor) or not t.is_cuda:
-        raise TypeError(f"{name} must be a CUDA tensor")
-    raise TypeError(f"{name} must be float32, float16 or bfloat16, got {t.dtype}")
-
-
-def _ints(t: torch.Tensor, dtype: torch.dtype, numel: int, name: str) -> None:
-    if not isinstance(t, torch.Tensor) or not t.is_cuda or t.dtype != dtype:
-        raise TypeError(f"{name} must be a CUDA tensor of {dtype}")
-    if t.numel() != numel or not t.is_contiguous():
-        raise ValueError(f"{name} must hold {numel} contiguous values")
-
-
-def _on(index: int, t: torch.Tensor, name: str) -> None:
-    if t.get_device() != index:
-        raise ValueError(f"{name} is on {t.device}, not on cuda:{index}")
-
-
-def _table(t: torch.Tensor, rows: int) -> tuple[int, int]:
-    """(columns, row stride) of a page table."""
-    if not isinstance(t, torch.Tensor) or t.dtype != torch.int32 or t.dim() != 2:
-        raise ValueError(f"table must be int32 [{rows}, cols] with contiguous rows")
-    (n, cols), (step, one) = t.shape, t.stride()
-    if n != rows or (cols > 1 and one != 1):
-        raise ValueError(f"table must be int32 [{rows}, cols] with contiguous rows")
-    return cols, step if step > cols else cols
+            return torch.empty(shape, dtype=dtype, device=device)
+    return torch.empty(shape, dtype=dtype, device=device)
 
 
 class Linear4:
@@ -110,7 +83,7 @@ class Linear4:
             self.device = codes.device
         self.d_in, self.d_out = d_in, d_out
         self._index = self.device.index
-        self._h = h
+        self._h, self._raw = h, h.value
 
     @staticmethod
     def _on_device(t: torch.Tensor) -> None:
@@ -137,27 +110,13 @@ class Linear4:
 
     def forward(self, x: torch.Tensor, out: torch.Tensor | None = None, stream=None) -> torch.Tensor:
         """x [B, d_in] or [d_in] (rows may be strided) -> [B, d_out] or [d_out] of x's type."""
-        dt = _act(x, "x")
-        index, shape, strides = self._index, x.shape, x.stride()
-        dim = len(shape)
-        if dim not in (1, 2) or shape[-1] != self.d_in or strides[-1] != 1:
-            raise ValueError(f"x must be [B, {self.d_in}] or [{self.d_in}] with contiguous rows, "
-                             f"got {tuple(shape)}")
-        _on(index, x, "x")
-        B, x_stride = (shape[0], strides[0]) if dim == 2 else (1, self.d_in)
-        out_stride = self.d_out
-        if out is None:
-            out = _empty(x, (B, out_stride) if dim == 2 else (out_stride,), x.dtype, stream)
-        else:
-            _on(index, out, "out")
-            if out.dtype != x.dtype or out.dim() != dim or out.shape[-1] != self.d_out \
-                    or out.stride(-1) != 1 or (dim == 2 and out.shape[0] != B):
-                raise ValueError(f"out must be {x.dtype} of {B} rows of {self.d_out} contiguous values")
-            if dim == 2:
-                out_stride = out.stride(0)
-        check(lib.prox_linear4_forward(self.handle, x.data_ptr(), x_stride, out.data_ptr(), out_stride, B, dt,
-                                       _raw_stream(stream, index)))
-        return out
+        if self._h is None:
+            raise RuntimeError("the weights are closed")
+        if stream is not None:
+            if out is None and isinstance(x, torch.Tensor):
+                out = _empty(self.device, x.shape[:-1] + (self.d_out,), x.dtype, stream)
+            stream = _raw_stream(stream, self._index)
+        return _decode4.linear4_forward(self._raw, self._index, self.d_in, self.d_out, x, out, stream)
 
     __call__ = forward
 
@@ -190,7 +149,7 @@ class KVCache4:
         check(lib.prox_kv4_create(k_codes.data_ptr(), k_scales.data_ptr(), v_codes.data_ptr(),
                                   v_scales.data_ptr(), self.num_pages, self.n_heads, self.page_size,
                                   self.head_dim, ctypes.byref(h)))
-        self._h = h
+        self._h, self._raw = h, h.value
 
     @classmethod
     def zeros(cls, num_pages: int, n_heads: int, page_size: int, head_dim: int,
@@ -228,35 +187,23 @@ class KVCache4:
     def append(self, k: torch.Tensor, v: torch.Tensor, slots: torch.Tensor, stream=None) -> None:
         """Quantises rows k, v [T, heads, head_dim] (any strides, values
         contiguous) into slots (int64 [T]; negative: skipped)."""
-        dt = _act(k, "k")
-        shape, ks, vs, index = k.shape, k.stride(), v.stride(), self._index
-        if len(shape) != 3 or shape[1] != self.n_heads or shape[2] != self.head_dim or v.shape != shape \
-                or ks[2] != 1 or vs[2] != 1:
-            raise ValueError(f"k and v must be [T, {self.n_heads}, {self.head_dim}] with contiguous rows")
-        if v.dtype != k.dtype:
-            raise TypeError(f"k and v must have one type, got {k.dtype} and {v.dtype}")
-        _ints(slots, torch.int64, shape[0], "slots")
-        _on(index, k, "k")
-        _on(index, v, "v")
-        _on(index, slots, "slots")
-        check(lib.prox_kv4_append(self.handle, k.data_ptr(), v.data_ptr(), ks[0], ks[1], vs[0], vs[1],
-                                  slots.data_ptr(), shape[0], dt, _raw_stream(stream, index)))
+        if self._h is None:
+            raise RuntimeError("the cache is closed")
+        _decode4.kv4_append(self._raw, self._index, self.n_heads, self.head_dim, k, v, slots,
+                            None if stream is None else _raw_stream(stream, self._index))
 
     def read(self, slots: torch.Tensor, dtype: torch.dtype = torch.float32,
              stream=None) -> tuple[torch.Tensor, torch.Tensor]:
         """The values held at slots (int64 [T]): k and v [T, heads, head_dim],
         zeros for negative slots."""
-        if dtype not in DTYPES:
-            raise TypeError(f"dtype must be float32, float16 or bfloat16, got {dtype}")
-        T = slots.numel()
-        _ints(slots, torch.int64, T, "slots")
-        _on(self._index, slots, "slots")
-        shape = (T, self.n_heads, self.head_dim)
-        k = _empty(slots, shape, dtype, stream)
-        v = torch.empty_like(k) if stream is None else _empty(slots, shape, dtype, stream)
-        check(lib.prox_kv4_read(self.handle, slots.data_ptr(), T, k.data_ptr(), v.data_ptr(), DTYPES[dtype],
-                                _raw_stream(stream, self._index)))
-        return k, v
+        if self._h is None:
+            raise RuntimeError("the cache is closed")
+        kv = None
+        if stream is not None:
+            shape = (slots.numel(), self.n_heads, self.head_dim)
+            kv = tuple(_empty(self.device, shape, dtype, stream) for _ in range(2))
+            stream = _raw_stream(stream, self._index)
+        return _decode4.kv4_read(self._raw, self._index, self.n_heads, self.head_dim, slots, dtype, kv, stream)
 
     def attend(self, q: torch.Tensor, table: torch.Tensor, lens: torch.Tensor, scale: float | None = None,
                out: torch.Tensor | None = None, lse: torch.Tensor | None = None, stream=None) -> torch.Tensor:
@@ -264,34 +211,14 @@ class KVCache4:
         [B, Hq, head_dim] for one token each; table int32 [B, cols] of pages;
         lens int32 [B], the cached tokens with the new ones among them.  scale
         defaults to head_dim ** -0.5.  lse: optional fp32 [B, Tq, Hq]."""
-        dt = _act(q, "q")
-        shape, strides, index = q.shape, q.stride(), self._index
-        dim = len(shape)
-        if dim not in (3, 4) or shape[-1] != self.head_dim or strides[-1] != 1:
-            raise ValueError(f"q must be [B, Tq, Hq, {self.head_dim}] or [B, Hq, {self.head_dim}] with "
-                             f"contiguous rows, got {tuple(shape)}")
-        B, Hq = shape[0], shape[-2]
-        Tq, q_tok = (shape[1], strides[1]) if dim == 4 else (1, 0)
-        cols, table_stride = _table(table, B)
-        _ints(lens, torch.int32, B, "lens")
-        _on(index, q, "q")
-        _on(index, table, "table")
-        _on(index, lens, "lens")
-        if out is None:
-            out = torch.empty_like(q) if stream is None and q.is_contiguous() else _empty(q, shape, q.dtype, stream)
-        else:
-            _on(index, out, "out")
-            if out.dtype != q.dtype or out.shape != shape or not out.is_contiguous():
-                raise ValueError("out must be a contiguous tensor of q's shape and type")
-        if lse is not None:
-            _on(index, lse, "lse")
-            if lse.dtype != torch.float32 or lse.numel() != B * Tq * Hq or not lse.is_contiguous():
-                raise ValueError(f"lse must hold {B * Tq * Hq} contiguous float32 values")
-        check(lib.prox_kv4_attend(self.handle, q.data_ptr(), strides[0], q_tok, strides[-2], Hq, B, Tq,
-                                  table.data_ptr(), table_stride, cols, lens.data_ptr(),
-                                  self._scale if scale is None else scale, out.data_ptr(),
-                                  None if lse is None else lse.data_ptr(), dt, _raw_stream(stream, index)))
-        return out
+        if self._h is None:
+            raise RuntimeError("the cache is closed")
+        if stream is not None:
+            if out is None and isinstance(q, torch.Tensor):
+                out = _empty(self.device, q.shape, q.dtype, stream)
+            stream = _raw_stream(stream, self._index)
+        return _decode4.kv4_attend(self._raw, self._index, self.head_dim, q, table, lens,
+                                   self._scale if scale is None else scale, out, lse, stream)
 
 
 class PagePlan(NamedTuple):
@@ -315,29 +242,13 @@ def plan_pages(lens: torch.Tensor, delta: torch.Tensor, table: torch.Tensor, fre
     place beyond what is in use; free_count: int32 [1].  commit: lens and
     free_count are updated in place too (and returned); otherwise the new ones
     are new tensors and the same plan may be made again."""
-    B = lens.numel()
-    _ints(lens, torch.int32, B, "lens")
-    _ints(delta, torch.int32, B, "delta")
-    _ints(free_count, torch.int32, 1, "free_count")
-    cap = free_pages.numel()
-    _ints(free_pages, torch.int32, cap, "free_pages")
-    cols, table_stride = _table(table, B)
-    if max_new < 0:
-        raise ValueError(f"max_new={max_new} must be >= 0")
-    index = lens.get_device()
-    for t, name in ((delta, "delta"), (table, "table"), (free_pages, "free_pages"), (free_count, "free_count")):
-        _on(index, t, name)
-    Linear4._on_device(lens)
-    buf = _empty(lens, (2 * B + 3 + max_new,), torch.int32, stream)
-    positions, new_lens, cu, count, status = buf.split_with_sizes([max_new, B, B + 1, 1, 1])
-    slots = _empty(lens, (max_new,), torch.int64, stream)
-    if commit:
-        new_lens, count = lens, free_count
-    check(lib.prox_plan_pages(lens.data_ptr(), delta.data_ptr(), B, int(page_size), table.data_ptr(), table_stride,
-                              cols, free_pages.data_ptr(), cap, free_count.data_ptr(), new_lens.data_ptr(),
-                              count.data_ptr(), cu.data_ptr(), slots.data_ptr(), positions.data_ptr(), max_new,
-                              status.data_ptr(), _raw_stream(stream, index)))
-    return PagePlan(new_lens, count, cu, slots, positions, status)
+    made = None
+    if stream is not None:
+        made = (_empty(lens.device, (2 * lens.numel() + 3 + max(0, max_new),), torch.int32, stream),
+                _empty(lens.device, (max(0, max_new),), torch.int64, stream))
+        stream = _raw_stream(stream, lens.device.index)
+    return PagePlan._make(_decode4.plan_pages(lens, delta, table, free_pages, free_count, page_size, max_new,
+                                              commit, made, stream))
 
 
 class Attention4:
