@@ -29,7 +29,7 @@
 namespace prox {
 namespace {
 
-constexpr int kMaxPlanCtas = 8;
+constexpr int kMaxPlanCtas = 16;  // beyond 8 a cluster needs the kernel's consent
 
 __device__ __forceinline__ void cluster_sync_all() {
   __syncwarp();
@@ -49,6 +49,35 @@ __device__ __forceinline__ int find_row(const int* pre, int n, int v) {
   return lo;
 }
 
+// Exclusive prefix sums of two values over the threads of the block, and their
+// totals.
+__device__ __forceinline__ void scan2(long long a, long long b, longlong2* scratch, long long* at_a, long long* at_b,
+                                      long long* all_a, long long* all_b) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
+  long long x = a, y = b;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const long long u = __shfl_up_sync(0xffffffffu, x, o), v = __shfl_up_sync(0xffffffffu, y, o);
+    if (lane >= o) x += u, y += v;
+  }
+  if (lane == 31) scratch[warp] = make_longlong2(x, y);
+  __syncthreads();
+  // every warp sums the warps before it
+  longlong2 w = lane < warps ? scratch[lane] : make_longlong2(0, 0);
+  long long before_x = lane < warp ? w.x : 0, before_y = lane < warp ? w.y : 0;
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) {
+    before_x += __shfl_xor_sync(0xffffffffu, before_x, o);
+    before_y += __shfl_xor_sync(0xffffffffu, before_y, o);
+    w.x += __shfl_xor_sync(0xffffffffu, w.x, o);
+    w.y += __shfl_xor_sync(0xffffffffu, w.y, o);
+  }
+  *at_a = before_x + x - a;
+  *at_b = before_y + y - b;
+  *all_a = w.x;
+  *all_b = w.y;
+}
+
 __global__ void __launch_bounds__(1024, 1) page_plan_kernel(PagePlan p, int ctas, int shift) {
   extern __shared__ int smem[];
   int* s_new = smem;                 // [B + 1] first new token of each request
@@ -56,7 +85,7 @@ __global__ void __launch_bounds__(1024, 1) page_plan_kernel(PagePlan p, int ctas
   int* s_drop = s_gain + p.B + 1;    // [B + 1] first page each request returns
   int* s_len = s_drop + p.B + 1;     // [B] before
   int* s_to = s_len + p.B;           // [B] after
-  __shared__ long long scratch[33];
+  __shared__ longlong2 scratch[33];
   pdl_wait();
   pdl_trigger();
   const int tid = threadIdx.x, per = (p.B + blockDim.x - 1) / blockDim.x;
@@ -79,9 +108,8 @@ __global__ void __launch_bounds__(1024, 1) page_plan_kernel(PagePlan p, int ctas
     n_new += to > len ? to - len : 0;
     n_page += need > have ? (long long)(need - have) << 32 : (long long)(have - need);
   }
-  long long all_new, all_page;
-  long long at_new = block_exclusive_scan(n_new, scratch, &all_new);
-  long long at_page = block_exclusive_scan(n_page, scratch, &all_page);
+  long long all_new, all_page, at_new, at_page;
+  scan2(n_new, n_page, scratch, &at_new, &at_page, &all_new, &all_page);
   const int taken = (int)(all_page >> 32), returned = (int)(all_page & 0xffffffffLL);
   const long long c1 = (long long)c0 + returned;
   bad |= c0 < 0 || c1 > p.free_cap || taken > c1 || all_new > p.max_new;
@@ -112,10 +140,13 @@ __global__ void __launch_bounds__(1024, 1) page_plan_kernel(PagePlan p, int ctas
     return j < c0 ? p.free_pages[j] : returned_page((int)(j - c0));
   };
   if (!bad) {
-    for (int n = at; n < returned; n += all) p.free_pages[c0 + n] = returned_page(n);
-    for (int n = at; n < taken; n += all) {
-      const int i = find_row(s_gain, p.B, n);
-      *entry(i, pages(s_len[i]) + (n - s_gain[i])) = taken_page(n);
+    for (int n = at; n < max(returned, taken); n += all) {  // both lookups before either write
+      const int back = n < returned ? returned_page(n) : 0;
+      if (n < taken) {
+        const int i = find_row(s_gain, p.B, n), id = taken_page(n);
+        *entry(i, pages(s_len[i]) + (n - s_gain[i])) = id;
+      }
+      if (n < returned) p.free_pages[c0 + n] = back;
     }
   }
   // The table is complete, and what lens_out and count_out may replace is read.
@@ -125,8 +156,9 @@ __global__ void __launch_bounds__(1024, 1) page_plan_kernel(PagePlan p, int ctas
     __syncthreads();
   const int lane = tid & 31;
   const bool sparse = total < 4 * p.B;  // few tokens a request: a search each beats the steps
-  for (int n0 = (at >> 5) * 128; n0 < p.max_new; n0 += all * 4) {
-    int i = n0 < total ? find_row(s_new, p.B, n0) : 0;
+  const int per_lane = p.max_new <= all ? 1 : 4;
+  for (int n0 = (at >> 5) * (32 * per_lane); n0 < p.max_new; n0 += all * per_lane) {
+    int i = !sparse && n0 < total ? find_row(s_new, p.B, n0) : 0;
     int pos[4], id[4];
     unsigned off[4];
 #pragma unroll
@@ -135,7 +167,7 @@ __global__ void __launch_bounds__(1024, 1) page_plan_kernel(PagePlan p, int ctas
       pos[k] = -1;
       id[k] = 0;
       off[k] = 0;
-      if (n < total) {
+      if (k < per_lane && n < total) {
         if (sparse)
           i = find_row(s_new, p.B, n);
         else
@@ -149,7 +181,7 @@ __global__ void __launch_bounds__(1024, 1) page_plan_kernel(PagePlan p, int ctas
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
       const int n = n0 + 32 * k + lane;
-      if (n >= p.max_new) break;
+      if (k >= per_lane || n >= p.max_new) break;
       p.slots[n] = pos[k] < 0 ? -1 : (long long)id[k] * page + off[k];
       p.positions[n] = pos[k];
     }
@@ -165,8 +197,10 @@ __global__ void __launch_bounds__(1024, 1) page_plan_kernel(PagePlan p, int ctas
 }  // namespace
 
 cudaError_t setup_page_plan() {
-  return cudaFuncSetAttribute(page_plan_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                              (5 * kPlanMaxRequests + 3) * 4);
+  cudaError_t e = cudaFuncSetAttribute(page_plan_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                       (5 * kPlanMaxRequests + 3) * 4);
+  if (e == cudaSuccess) e = cudaFuncSetAttribute(page_plan_kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+  return e;
 }
 
 cudaError_t launch_page_plan(const PagePlan& p, cudaStream_t s) {
