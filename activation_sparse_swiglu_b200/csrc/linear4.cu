@@ -169,7 +169,7 @@ __global__ void __launch_bounds__(warps_of(NT) * 32, 1) linear4_kernel(const Lin
   // x at input rows 2, 3 mod 4, whose codes stand at 6-9, against rows 0, 1
   constexpr float kHigh = ALL_HIGH ? 1.f : 0.0625f;
   extern __shared__ __align__(16) char smem[];
-  __shared__ int2 s_cut[kWarps];
+  __shared__ int2 s_cut[kWarps];  // of warps 0 .. W - 2; the last entry: a bit for each that is cut
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int g = lane >> 2, t = lane & 3;
   const int rank = a.cluster > 1 ? (int)cluster_rank() : 0;
@@ -221,12 +221,17 @@ __global__ void __launch_bounds__(warps_of(NT) * 32, 1) linear4_kernel(const Lin
     const int W = min(U, kWarps);
     const int beg = warp < W ? range_at(U, warp, W) : U, end = warp < W ? range_at(U, warp + 1, W) : U;
     if (ph > 0) __syncthreads();  // x and the parts of the phase before have been read
-    if (threadIdx.x < W - 1) {
+    if (warp == 0) {
       // the strip that starts in warp w0's range and goes on past it, and the
       // warp that it ends in
-      const int w0 = threadIdx.x, from = range_at(U, w0 + 1, W), s = from / nG;
-      const bool cut = from != s * nG && range_at(U, w0, W) <= s * nG;
-      s_cut[w0] = make_int2(cut ? s : -1, cut ? range_of(U, s * nG + nG - 1, W) : 0);
+      bool cut = false;
+      if (lane < W - 1) {
+        const int from = range_at(U, lane + 1, W), s = from / nG;
+        cut = from != s * nG && range_at(U, lane, W) <= s * nG;
+        if (cut) s_cut[lane] = make_int2(s, range_of(U, s * nG + nG - 1, W));
+      }
+      const unsigned cuts = __ballot_sync(0xffffffffu, cut);
+      if (lane == 0) s_cut[kWarps - 1].x = (int)cuts;
     }
 
     // Every lane copies the very bytes it will read, so its own wait is all the
@@ -266,33 +271,52 @@ __global__ void __launch_bounds__(warps_of(NT) * 32, 1) linear4_kernel(const Lin
     // lanes a group, a warp 32 / LPG groups of a token.
     constexpr int LPG = DT == PROX_F32 ? 8 : 4, GPW = 32 / LPG;
     const int runs = (nG + GPW - 1) / GPW;
-    for (int b = 0, run = warp; b < a.B && runs > 0;) {
-      if (run >= runs) {
-        run -= runs;
-        ++b;
-        continue;
-      }
-      const int gr = run * GPW + lane / LPG;
-      const int turn = DT == PROX_F32 ? (lane >> 2) & 3 : (lane >> 1) & 3;
-      run += kWarps;
+    const int turn = DT == PROX_F32 ? (lane >> 2) & 3 : (lane >> 1) & 3;
+    struct Item {
+      int b, run;
       uint4 raw[4];
-      const T* src = static_cast<const T*>(a.x) + b * a.x_stride + (int64_t)(pg0 + gr) * kGroupRows +
+    };
+    auto settle = [&](Item& it) {
+      while (it.run >= runs && it.b < a.B) it.run -= runs, ++it.b;
+    };
+    auto fetch = [&](Item& it) {
+      const int gr = it.run * GPW + lane / LPG;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) it.raw[j] = make_uint4(0, 0, 0, 0);
+      if (it.b >= a.B || gr >= nG) return;
+      const T* src = static_cast<const T*>(a.x) + it.b * a.x_stride + (int64_t)(pg0 + gr) * kGroupRows +
                      (lane % LPG) * (64 / (int)sizeof(T));
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
         const T* p = src + ((j + turn) & 3) * (16 / (int)sizeof(T));
-        raw[j] = make_uint4(0, 0, 0, 0);
-        if (gr < nG) {
-          if (a.x_vec) {
-            raw[j] = *reinterpret_cast<const uint4*>(p);
-          } else {
-            T v[16 / sizeof(T)];
+        if (a.x_vec) {
+          it.raw[j] = *reinterpret_cast<const uint4*>(p);
+        } else {
+          T v[16 / sizeof(T)];
 #pragma unroll
-            for (int i = 0; i < (int)(16 / sizeof(T)); ++i) v[i] = p[i];
-            memcpy(&raw[j], v, 16);
-          }
+          for (int i = 0; i < (int)(16 / sizeof(T)); ++i) v[i] = p[i];
+          memcpy(&it.raw[j], v, 16);
         }
       }
+    };
+    // the loads of two items are in flight while a third is converted
+    Item ahead[2];
+    ahead[0].b = runs > 0 ? 0 : a.B;
+    ahead[0].run = warp;
+    settle(ahead[0]);
+    fetch(ahead[0]);
+    ahead[1].b = ahead[0].b;
+    ahead[1].run = ahead[0].run + kWarps;
+    settle(ahead[1]);
+    fetch(ahead[1]);
+    while (ahead[0].b < a.B) {
+      const Item now = ahead[0];
+      ahead[0] = ahead[1];
+      ahead[1].run += kWarps;
+      settle(ahead[1]);
+      fetch(ahead[1]);
+      const int b = now.b, gr = now.run * GPW + lane / LPG;
+      const uint4(&raw)[4] = now.raw;
       float mx = fmaxf(fmaxf(top<DT>(raw[0]), top<DT>(raw[1])), fmaxf(top<DT>(raw[2]), top<DT>(raw[3])));
 #pragma unroll
       for (int o = LPG / 2; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
@@ -454,9 +478,8 @@ __global__ void __launch_bounds__(warps_of(NT) * 32, 1) linear4_kernel(const Lin
     // strips that several warps share, in warp order: the strip at the start of
     // warp w's range, where w is the second to have a part of it; neighbouring
     // threads take neighbouring channels of one token
-    for (int w0 = 0; w0 < W - 1; ++w0) {  // w = w0 + 1
-      const int s = s_cut[w0].x, wb = s_cut[w0].y;
-      if (s < 0) continue;
+    for (unsigned cuts = s_cut[kWarps - 1].x; cuts; cuts &= cuts - 1) {
+      const int w0 = __ffs(cuts) - 1, s = s_cut[w0].x, wb = s_cut[w0].y;  // w = w0 + 1
       for (int e = threadIdx.x; e < kStrip * a.B; e += kThreads) {
         const int row = e % kStrip, b = e / kStrip;
         float v = tail(w0)[b * kPartRow + row];
