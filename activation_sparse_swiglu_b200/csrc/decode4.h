@@ -93,7 +93,8 @@ struct PagePlan {
   int max_new = 0;
   int32_t* status = nullptr;
 };
-cudaError_t setup_page_plan();
-cudaError_t launch_page_plan(const PagePlan& p, cudaStream_t s);
+// Loads the kernel and finds the largest cluster (CTAs) the device can hold.
+cudaError_t setup_page_plan(int* max_ctas);
+cudaError_t launch_page_plan(const PagePlan& p, int max_ctas, cudaStream_t s);
 
 }  // namespace prox

@@ -1,8 +1,8 @@
 // C ABI of the 4-bit operators: argument checks, the linear4 and kv4 handles,
 // and their launches.
+#include <atomic>
 #include <climits>
 #include <cmath>
-#include <mutex>
 #include <new>
 
 #include "api_util.h"
@@ -245,8 +245,8 @@ prox_status prox_kv4_error(prox_kv4* C, int32_t* word_host, void* stream) {
 static prox_status check_rows(const prox_kv4* C, const int64_t* slots, int T, int dtype) {
   if (!C) return fail(PROX_EINVAL, "kv4 handle is NULL");
   if (!good_dtype(dtype)) return fail(PROX_EINVAL, "dtype %d is not one of PROX_F32, PROX_F16, PROX_BF16", dtype);
-  if (T < 0 || (int64_t)T * C->heads * 16 > (int64_t)INT_MAX * 128)
-    return fail(PROX_EINVAL, "T=%d is negative or too large", T);
+  if (T < 0 || (int64_t)T * C->heads > INT_MAX)
+    return fail(PROX_EINVAL, "T=%d must be >= 0 and T * n_heads below 2^31", T);
   if (T > 0 && (!slots || !aligned(slots, 8))) return fail(PROX_EINVAL, "slots must be an 8-byte aligned pointer");
   return on_device(C->device, "kv4 cache");
 }
@@ -335,11 +335,13 @@ prox_status prox_plan_pages(const int32_t* lens, const int32_t* delta, int B, in
   int dev, sms;
   prox_status st = check_device(&dev, &sms);
   if (st != PROX_OK) return st;
-  static std::once_flag once[kMaxDevices];
-  cudaError_t e = cudaSuccess;
   if (dev >= kMaxDevices) return fail(PROX_EUNSUPPORTED, "device ordinal %d out of range", dev);
-  std::call_once(once[dev], [&] { e = prox::setup_page_plan(); });
-  PROX_CUDA(e, "prox_plan_pages set-up");
+  static std::atomic<int> ctas_of[kMaxDevices];  // largest cluster, 0: not set up yet
+  int ctas = ctas_of[dev].load(std::memory_order_acquire);
+  if (ctas == 0) {
+    PROX_CUDA(prox::setup_page_plan(&ctas), "prox_plan_pages set-up");
+    ctas_of[dev].store(ctas, std::memory_order_release);
+  }
   prox::PagePlan p;
   p.lens = lens;
   p.delta = delta;
@@ -358,7 +360,7 @@ prox_status prox_plan_pages(const int32_t* lens, const int32_t* delta, int B, in
   p.positions = positions;
   p.max_new = max_new;
   p.status = status;
-  PROX_CUDA(prox::launch_page_plan(p, as_stream(stream)), "prox_plan_pages launch");
+  PROX_CUDA(prox::launch_page_plan(p, ctas, as_stream(stream)), "prox_plan_pages launch");
   return PROX_OK;
 }
 

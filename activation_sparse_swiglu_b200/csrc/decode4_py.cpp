@@ -96,7 +96,8 @@ const at::Tensor& ints(PyObject* o, int index, at::ScalarType type, int64_t nume
 const at::Tensor& page_table(PyObject* o, int index, int64_t rows, int64_t* cols, int64_t* stride) {
   if (!THPVariable_Check(o)) RAISE(PyExc_TypeError, "table must be a CUDA tensor");
   const at::Tensor& t = THPVariable_Unpack(o);
-  if (t.scalar_type() != at::kInt || t.dim() != 2 || t.size(0) != rows || (t.size(1) > 1 && t.stride(1) != 1))
+  if (t.scalar_type() != at::kInt || t.dim() != 2 || t.size(0) != rows || (t.size(1) > 1 && t.stride(1) != 1) ||
+      (rows > 1 && t.stride(0) < t.size(1)))
     RAISE(PyExc_ValueError, "table must be int32 [%lld, cols] with contiguous rows", (long long)rows);
   tensor(o, "table");
   on(t, index, "table");

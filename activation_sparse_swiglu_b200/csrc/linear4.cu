@@ -598,7 +598,7 @@ size_t ring_bytes(int nt, int depth) { return (size_t)warps_of(nt) * depth * kSl
 // 43.
 constexpr double kJoin[4] = {0, 35, 45, 75};
 
-bool plan_linear4(const prox_linear4* L, int B, int dtype, Plan* best) {
+bool plan_linear4(const prox_linear4* L, int strips, int B, int dtype, Plan* best) {
   const int nt = col_tiles(B, dtype), parts = dtype == PROX_F32 ? 2 : 1;
   const int cols = B * parts, tb = 8 * nt / parts;
   double least = 1e300;
@@ -607,9 +607,9 @@ bool plan_linear4(const prox_linear4* L, int B, int dtype, Plan* best) {
     if (L->clusters[ci] < 1 || (c > 1 && c > L->G)) continue;
     Plan p;
     p.cluster = c;
-    p.clusters = L->strips < L->clusters[ci] ? L->strips : L->clusters[ci];
-    p.per_clus = (L->strips + p.clusters - 1) / p.clusters;
-    p.clusters = (L->strips + p.per_clus - 1) / p.per_clus;
+    p.clusters = strips < L->clusters[ci] ? strips : L->clusters[ci];
+    p.per_clus = (strips + p.clusters - 1) / p.clusters;
+    p.clusters = (strips + p.per_clus - 1) / p.per_clus;
     p.per_rank = (L->G + c - 1) / c;
     p.per_phase = p.per_rank;
     auto front = [&] {  // everything before the rings
@@ -674,41 +674,55 @@ cudaError_t setup_linear4(prox_linear4* L) {
 
 cudaError_t launch_linear4(const prox_linear4* L, const void* x, int64_t x_stride, void* out, int64_t out_stride,
                            int B, int dtype, cudaStream_t s) {
+  // All strips in one launch, unless x takes several phases (or a cluster) and
+  // the results that are then kept in shared memory do not fit: fewer strips a
+  // launch.  (16 fp32 tokens over some 10^5 channels or more.)
   Plan p;
-  if (!plan_linear4(L, B, dtype, &p)) return cudaErrorInvalidConfiguration;
-  const int nt = col_tiles(B, dtype);
+  int chunk = L->strips;
+  while (!plan_linear4(L, chunk, B, dtype, &p)) {
+    if (chunk == 1) return cudaErrorInvalidConfiguration;
+    chunk = (chunk + 1) / 2;
+  }
+  const int nt = col_tiles(B, dtype), size = dtype == PROX_F32 ? 4 : 2;
   LinearArgs a;
-  a.codes = reinterpret_cast<const char*>(L->codes);
-  a.scales = reinterpret_cast<const char*>(L->scales);
   a.x = x;
   a.x_stride = x_stride;
-  a.out = out;
   a.out_stride = out_stride;
   a.B = B;
-  a.N = L->N;
   a.G = L->G;
-  a.strips = L->strips;
-  a.per_clus = p.per_clus;
-  a.per_rank = p.per_rank;
-  a.per_phase = p.per_phase;
-  a.cluster = p.cluster;
-  a.ring_at = (int)p.ring_at;
-  a.x_vec = (reinterpret_cast<uintptr_t>(x) & 15) == 0 && (B == 1 || x_stride % (dtype == PROX_F32 ? 4 : 8) == 0);
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)(p.clusters * p.cluster), 1, 1);
-  cfg.blockDim = dim3(warps_of(nt) * 32, 1, 1);
-  cfg.dynamicSmemBytes = p.smem;
-  cfg.stream = s;
-  cudaLaunchAttribute attr[2];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  attr[1].id = cudaLaunchAttributeClusterDimension;
-  attr[1].val.clusterDim.x = p.cluster;
-  attr[1].val.clusterDim.y = 1;
-  attr[1].val.clusterDim.z = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = p.cluster > 1 ? 2 : 1;
-  return cudaLaunchKernelEx(&cfg, pick(dtype, nt, p.depth), a);
+  a.x_vec = (reinterpret_cast<uintptr_t>(x) & 15) == 0 && (B == 1 || x_stride % (16 / size) == 0);
+  for (int first = 0; first < L->strips; first += chunk) {
+    if (L->strips - first < chunk && !plan_linear4(L, L->strips - first, B, dtype, &p))
+      return cudaErrorInvalidConfiguration;
+    a.codes = reinterpret_cast<const char*>(L->codes) + (size_t)first * L->G * kCodeBytes;
+    a.scales = reinterpret_cast<const char*>(L->scales) + (size_t)first * L->G * kScaleBytes;
+    a.out = static_cast<char*>(out) + (size_t)first * kStrip * size;
+    a.N = L->N - first * kStrip;
+    a.strips = L->strips - first < chunk ? L->strips - first : chunk;
+    if (a.strips == chunk && first + chunk < L->strips) a.N = chunk * kStrip;
+    a.per_clus = p.per_clus;
+    a.per_rank = p.per_rank;
+    a.per_phase = p.per_phase;
+    a.cluster = p.cluster;
+    a.ring_at = (int)p.ring_at;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)(p.clusters * p.cluster), 1, 1);
+    cfg.blockDim = dim3(warps_of(nt) * 32, 1, 1);
+    cfg.dynamicSmemBytes = p.smem;
+    cfg.stream = s;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = p.cluster;
+    attr[1].val.clusterDim.y = 1;
+    attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = p.cluster > 1 ? 2 : 1;
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, pick(dtype, nt, p.depth), a);
+    if (e != cudaSuccess) return e;
+  }
+  return cudaSuccess;
 }
 
 }  // namespace prox

@@ -196,16 +196,31 @@ __global__ void __launch_bounds__(1024, 1) page_plan_kernel(PagePlan p, int ctas
 
 }  // namespace
 
-cudaError_t setup_page_plan() {
-  cudaError_t e = cudaFuncSetAttribute(page_plan_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                       (5 * kPlanMaxRequests + 3) * 4);
+cudaError_t setup_page_plan(int* max_ctas) {
+  const size_t smem = (5 * kPlanMaxRequests + 3) * 4;
+  cudaError_t e = cudaFuncSetAttribute(page_plan_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
   if (e == cudaSuccess) e = cudaFuncSetAttribute(page_plan_kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
-  return e;
+  if (e != cudaSuccess) return e;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(kMaxPlanCtas, 1, 1);
+  cfg.blockDim = dim3(1024, 1, 1);
+  cfg.dynamicSmemBytes = smem;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = kMaxPlanCtas;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  int n = 0;
+  if (cudaOccupancyMaxActiveClusters(&n, page_plan_kernel, &cfg) != cudaSuccess) cudaGetLastError(), n = 0;
+  *max_ctas = n > 0 ? kMaxPlanCtas : 8;  // eight are portable
+  return cudaSuccess;
 }
 
-cudaError_t launch_page_plan(const PagePlan& p, cudaStream_t s) {
+cudaError_t launch_page_plan(const PagePlan& p, int max_ctas, cudaStream_t s) {
   int ctas = 1;
-  while (ctas < kMaxPlanCtas && (p.max_new > 4096 * ctas || p.B > 2048 * ctas)) ctas *= 2;
+  while (ctas < max_ctas && (p.max_new > 4096 * ctas || p.B > 2048 * ctas)) ctas *= 2;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(ctas, 1, 1);
   cfg.blockDim = dim3(p.max_new <= 256 && p.B <= 256 ? 256 : 1024, 1, 1);

@@ -260,7 +260,7 @@ class Attention4:
     values), w_o: bf16 [n_heads head_dim, d]; quantised by pack_proxy's rule.
     rotate: optional callable (q, k, positions) -> (q, k) that applies the
     model's position encoding to q [n, n_heads, head_dim] and k [n, n_kv_heads,
-    head_dim].  The cache has num_pages pages of page_size tokens; which rows a
+    head_dim] (on the step's stream).  The cache has num_pages pages of page_size tokens; which rows a
     step's tokens take is the caller's plan (plan_pages), shared by all layers.
     """
 
@@ -283,7 +283,8 @@ class Attention4:
         heads = self.qkv.forward(x, stream=stream).view(B, self.n_heads + 2 * self.n_kv_heads, D)
         q, k, v = heads.split_with_sizes([self.n_heads, self.n_kv_heads, self.n_kv_heads], 1)
         if self.rotate is not None:
-            q, k = self.rotate(q, k, plan.positions[:B])
+            with torch.cuda.stream(stream if isinstance(stream, torch.cuda.Stream) else None):
+                q, k = self.rotate(q, k, plan.positions[:B])
         self.cache.append(k, v, plan.slots[:B], stream=stream)
         o = self.cache.attend(q, table, plan.lens, stream=stream)
         return self.out.forward(o.view(B, self.n_heads * D), stream=stream)

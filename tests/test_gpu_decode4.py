@@ -179,6 +179,28 @@ def test_linear4_two_streams_and_graph(prox):
         assert torch.equal(out, w)
 
 
+@pytest.mark.parametrize("dtype, B", [(torch.float32, 16), (torch.bfloat16, 16), (torch.float32, 7)])
+def test_linear4_largest_outputs_with_many_columns(prox, dtype, B):
+    """Where x needs several passes and the results of all channels would not
+    stay in shared memory: more channels than one launch takes."""
+    K, N = 8192, (1 << 19) + 34
+    codes, scales, x = linear_case(prox, K, N, B, dtype, seed=21)
+    y = prox.Linear4(codes=codes, scales=scales)(x)
+    for n0 in list(range(0, N, 1 << 16)) + [N - 34]:
+        n1 = min(N, n0 + 2050)
+        part = codes[:, n0 // 2:n1 // 2].contiguous(), scales[:, n0:n1].contiguous()
+        want, tol = ref.linear4(x, *part)
+        within(y[:, n0:n1], want, tol)
+    # and everywhere against the same weights in narrow slices
+    for n0 in range(0, N, 1 << 17):
+        n1 = min(N, n0 + (1 << 17))
+        sl = prox.Linear4(codes=codes[:, n0 // 2:n1 // 2].contiguous(), scales=scales[:, n0:n1].contiguous())(x)
+        diff = (sl.double() - y[:, n0:n1].double()).norm() / sl.double().norm()
+        assert diff <= (2e-6 if dtype == torch.float32 else 2.0 ** -8)
+        sl_bad = (sl - y[:, n0:n1]).abs().amax(0) > 0.05 * sl.abs().amax()
+        assert not sl_bad.any()
+
+
 # ---- the cache's rows ----------------------------------------------------------
 
 def new_cache(prox, pages, heads, page, dim):
@@ -275,6 +297,10 @@ def test_append_slots_past_the_cache(prox):
     assert cache.error_word() == prox.DEVERR_SLOT
     assert rk[0].ne(0).all() and (rk[1:] == 0).all()
     assert (cache.k_scales.flatten()[1:] == 0).all()
+    wide = torch.ones((1, 1, 64), device="cuda").expand(4, 1, 64)  # a row for every token
+    cache.append(wide, wide, torch.tensor([1, 2, 3, 4], device="cuda"))
+    assert (cache.read(torch.arange(1, 5, device="cuda"))[0] == rk[:1]).all()
+    cache.k_scales.view(-1)[1:5] = 0
     cache.append(k[:0], k[:0], slots[:0])
     assert cache.read(slots[:0])[0].shape == (0, 1, 64)
     with pytest.raises(TypeError):
@@ -488,6 +514,9 @@ def test_attend_refusals(prox):
         cache.attend(q, table, lens, out=torch.empty_like(q).float())
     with pytest.raises(ValueError):
         cache.attend(q, table, lens, lse=torch.empty(1, device="cuda"))
+    # rows that share memory could not be told apart
+    with pytest.raises(ValueError, match="contiguous rows"):
+        cache.attend(q.expand(2, -1, -1, -1), table.expand(2, -1), lens.repeat(2))
     # no columns at all: every length but 0 is out of range
     zero = torch.zeros_like(lens)
     assert (cache.attend(q, table[:, :0], zero) == 0).all() and cache.error_word() == 0
@@ -578,6 +607,12 @@ def test_plan_pages_exact_fit_and_refusals(prox):
     assert not run_plan(prox, [0, 0], [1, 0], 4, 16, free, -1, 64)          # a count below 0
     assert not run_plan(prox, [0, 5], [2 ** 31 - 1, 2 ** 31 - 1], 4, 16, free, 3, 64)
     assert run_plan(prox, [0, 0], [0, 0], 0, 16, [], 0, 0, table=[[], []])
+
+
+def test_plan_pages_refuses_rows_that_share_memory(prox):
+    i32 = lambda x: torch.tensor(x, dtype=torch.int32, device="cuda")  # noqa: E731
+    with pytest.raises(ValueError, match="contiguous rows"):
+        prox.plan_pages(i32([0, 0]), i32([1, 1]), i32([[0, 0]]).expand(2, -1), i32([5, 6]), i32([2]), 16, max_new=2)
 
 
 def test_plan_pages_strided_table_and_max_new_zero(prox):
