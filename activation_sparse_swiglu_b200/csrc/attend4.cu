@@ -21,14 +21,15 @@
 // fp16 and bf16 queries: a nibble masked out of a word is an fp16 subnormal
 // (spread8), 5/8 of an instruction per code; the offset 8 is taken off in the
 // sums' start values: -8 sum_d Q_d for a score, and -8 sum_j p_j for an output,
-// which one product with a constant gives in the right registers.  The
-// cancellation costs a few fp32 roundings of 8 sum p, invisible in a 16-bit
-// result.  fp32 queries are held to fp32: their codes are widened to exact
+// which one product with a constant gives in the right registers.  Such
+// sums are then good to 2^-14 of a code step of the largest factor (see
+// spread8), a quarter of what rounding a probability to 11 bits costs.  fp32
+// queries are held to fp32: their codes are widened to exact
 // integers (9/8 instructions), queries and probabilities split into hi + lo
 // columns.  bf16 and fp32 queries are scaled by a power of two.  (Exact
 // widening for all types, 32 rows a step and a page lookup per 16-byte copy
 // took 1080 instructions per 32 rows and 132 us for 64 requests of the
-// 8B-shaped model, 0.35 of the copy bandwidth.)
+// 8B-shaped model; it is 555 now and 80 us, the loop itself at 5 TB/s.)
 // Probabilities times vs are scaled by a power of two per step so that they
 // use fp16's range; each step's product starts afresh and joins the fp32
 // output with one fused multiply-add, so the tensor core's own sums stay short.
@@ -164,6 +165,7 @@ __global__ void __launch_bounds__(warps_of(D, NT, parts_of(DT)) * 32, 1) attend4
   __shared__ int s_head_at[kMaxWarps], s_tail_at[kMaxWarps];  // 0: none; else kOpen, kDone, kEarly
   __shared__ Chain s_chain[kMaxWarps + 1];
   __shared__ int s_chains, s_last[2];
+  __shared__ int2 s_ctas[2];  // the CTAs that share those contexts
   constexpr int kOpen = 1, kDone = 2, kEarly = 3;  // goes on; ends with the range; ends before it
 
   pdl_wait();
@@ -767,25 +769,30 @@ __global__ void __launch_bounds__(warps_of(D, NT, parts_of(DT)) * 32, 1) attend4
   __syncthreads();
   const int chains = s_chains;
   if (chains == 0) return;
-  constexpr int kSlices = RB * (D / 4);  // of four values, of a part
-  // parts added one by one to a row's maximum, sum and four values
-  auto result = [&](const Cursor& s, int row, int d, float top, float l, float(&y)[4], float* to) {
+  // A thread joins NV runs of four values of one row, D / 16 NV threads a row
+  // (neighbours take neighbouring runs).
+  auto result = [&](const Cursor& s, int row, int d0, int apart, float top, float l, auto& y, float* to) {
+    constexpr int NV = sizeof(y) / sizeof(y[0]);
     if (to) {
-      store_vals<PROX_F32, 4>(to + row * D + d, true, y);
-      if (d == 0) to[RB * D + row] = top, to[RB * D + RB + row] = l;
+#pragma unroll
+      for (int j = 0; j < NV; ++j) store_vals<PROX_F32, 4>(to + row * D + d0 + j * apart, true, y[j]);
+      if (d0 == 0) to[RB * D + row] = top, to[RB * D + RB + row] = l;
       return;
     }
     const int64_t o = out_at(s, row);
     if (o < 0) return;
     const float f = l == 0.f ? 0.f : 1.f / l;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) y[i] *= f;
-    store_vals<DT, 4>(static_cast<T*>(c.out) + o + d, true, y);
-    if (c.lse && d == 0) c.lse[o / D] = l == 0.f ? -INFINITY : 0.6931471805599453f * (top + log2f(l));
+    for (int j = 0; j < NV; ++j) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) y[j][i] *= f;
+      store_vals<DT, 4>(static_cast<T*>(c.out) + o + d0 + j * apart, true, y[j]);
+    }
+    if (c.lse && d0 == 0) c.lse[o / D] = l == 0.f ? -INFINITY : 0.6931471805599453f * (top + log2f(l));
   };
   // adds parts with maxima m (-inf: none), sums q and values o to top, l and y
-  auto add_parts = [](const auto& m, const auto& q, const auto& o, float* top, float* l, float(&y)[4]) {
-    constexpr int n = sizeof(m) / sizeof(m[0]);
+  auto add_parts = [](const auto& m, const auto& q, const auto& o, float* top, float* l, auto& y) {
+    constexpr int n = sizeof(m) / sizeof(m[0]), NV = sizeof(y) / sizeof(y[0]);
     float up = *top;
 #pragma unroll
     for (int i = 0; i < n; ++i) up = fmaxf(up, m[i]);
@@ -794,40 +801,48 @@ __global__ void __launch_bounds__(warps_of(D, NT, parts_of(DT)) * 32, 1) attend4
     *top = up;
     *l *= f;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) y[i] *= f;
+    for (int j = 0; j < NV; ++j)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) y[j][i] *= f;
 #pragma unroll
     for (int i = 0; i < n; ++i) {
       f = exp2_fast(m[i] - base);  // 0 without a visible row (a NaN in the part stays)
       *l = fmaf(q[i], f, *l);
-      y[0] = fmaf(o[i].x, f, y[0]), y[1] = fmaf(o[i].y, f, y[1]);
-      y[2] = fmaf(o[i].z, f, y[2]), y[3] = fmaf(o[i].w, f, y[3]);
+#pragma unroll
+      for (int j = 0; j < NV; ++j) {
+        y[j][0] = fmaf(o[i][j].x, f, y[j][0]), y[j][1] = fmaf(o[i][j].y, f, y[j][1]);
+        y[j][2] = fmaf(o[i][j].z, f, y[j][2]), y[j][3] = fmaf(o[i][j].w, f, y[j][3]);
+      }
     }
   };
-  for (int e = threadIdx.x; e < chains * kSlices; e += blockDim.x) {
-    const Chain& ch = s_chain[e / kSlices];
-    const int row = e % kSlices / (D / 4), d = e % (D / 4) * 4;
+  const float4 zero4 = make_float4(0.f, 0.f, 0.f, 0.f);
+  constexpr int kRuns = D / 16;  // threads of a row, four runs each
+  for (int e = threadIdx.x; e < chains * RB * kRuns; e += blockDim.x) {
+    const Chain& ch = s_chain[e / (RB * kRuns)];
+    const int row = e / kRuns % RB, d0 = e % kRuns * 4;
     auto part = [&](int w) -> const float* {  // the chain's part in warp w, NULL: none
       if (w == ch.first && !ch.from_head) return ring_part(w);
       if (!s_head_at[w]) return nullptr;
       return s_head_at[w] == kEarly ? warp_parts + (size_t)w * SLOT : ring_part(w);
     };
     // (four parts' loads at once: some lie in global memory)
-    float top = -INFINITY, l = 0.f, y[4] = {};
+    float top = -INFINITY, l = 0.f, y[4][4] = {};
     for (int w0 = ch.first; w0 <= ch.last; w0 += 4) {
-      const float* p[4];
       float m[4], q[4];
-      float4 o[4];
+      float4 o[4][4];
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        p[i] = w0 + i <= ch.last ? part(w0 + i) : nullptr;
-        m[i] = p[i] ? p[i][RB * D + row] : -INFINITY;
-        q[i] = p[i] ? p[i][RB * D + RB + row] : 0.f;
-        o[i] = p[i] ? *reinterpret_cast<const float4*>(p[i] + row * D + d) : make_float4(0.f, 0.f, 0.f, 0.f);
+        const float* p = w0 + i <= ch.last ? part(w0 + i) : nullptr;
+        m[i] = p ? p[RB * D + row] : -INFINITY;
+        q[i] = p ? p[RB * D + RB + row] : 0.f;
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+          o[i][j] = p ? *reinterpret_cast<const float4*>(p + row * D + d0 + j * (D / 4)) : zero4;
       }
       add_parts(m, q, o, &top, &l, y);
     }
     const bool left = ch.s.beg < cb;  // began in an earlier CTA
-    result(ch.s, row, d, top, l, y,
+    result(ch.s, row, d0, D / 4, top, l, y,
            left || ch.right ? a.part + (size_t)(2 * blockIdx.x + (left ? 0 : 1)) * SLOT : nullptr);
   }
   bool shared = false;
@@ -836,12 +851,6 @@ __global__ void __launch_bounds__(warps_of(D, NT, parts_of(DT)) * 32, 1) attend4
   // the last CTA to leave its part of a context joins them all
   __threadfence();
   __syncthreads();
-  auto ctas = [&](const Cursor& s, int* c0, int* c1) {
-    const long long first = (long long)H * pre[s.b] + (long long)(s.head * a.blocks + s.block) * (s.n + kStartUnits) +
-                            kStartUnits;  // the place behind the context's start
-    *c0 = (int)(((first + 1) * P - 1) / places);
-    *c1 = (int)(((first + s.n) * P - 1) / places);
-  };
   if (threadIdx.x < 2) {  // the context from the left, the one that goes on to the right
     int found = -1;
     for (int i = 0; i < chains; ++i) {
@@ -849,8 +858,12 @@ __global__ void __launch_bounds__(warps_of(D, NT, parts_of(DT)) * 32, 1) attend4
       if (threadIdx.x == 0 ? left : !left && s_chain[i].right) found = i;
     }
     if (found >= 0) {
-      int c0, c1;
-      ctas(s_chain[found].s, &c0, &c1);
+      const Cursor& s = s_chain[found].s;
+      const long long first = (long long)H * pre[s.b] +
+                              (long long)(s.head * a.blocks + s.block) * (s.n + kStartUnits) +
+                              kStartUnits;  // the place behind the context's start
+      const int c0 = (int)(((first + 1) * P - 1) / places), c1 = (int)(((first + s.n) * P - 1) / places);
+      s_ctas[threadIdx.x] = make_int2(c0, c1);
       if (atomicAdd(a.arrived + c0, 1) == c1 - c0)
         a.arrived[c0] = 0;  // for the next call
       else
@@ -859,31 +872,30 @@ __global__ void __launch_bounds__(warps_of(D, NT, parts_of(DT)) * 32, 1) attend4
     s_last[threadIdx.x] = found;
   }
   __syncthreads();
+  if (s_last[0] < 0 && s_last[1] < 0) return;
+  __threadfence();
+  constexpr int kSlices = RB * (D / 4);
 #pragma unroll
   for (int k = 0; k < 2; ++k) {
     if (s_last[k] < 0) continue;
-    __threadfence();
-    const Cursor s = s_chain[s_last[k]].s;
-    int c0, c1;
-    ctas(s, &c0, &c1);
-    auto part = [&](int cta) { return a.part + (size_t)(2 * cta + (cta == c0 ? 1 : 0)) * SLOT; };
+    const int c0 = s_ctas[k].x, c1 = s_ctas[k].y;
     for (int e = threadIdx.x; e < kSlices; e += blockDim.x) {
       const int row = e / (D / 4), d = e % (D / 4) * 4;
-      float top = -INFINITY, l = 0.f, y[4] = {};
+      float top = -INFINITY, l = 0.f, y[1][4] = {};
       for (int i0 = c0; i0 <= c1; i0 += 8) {
         float m[8], q[8];
-        float4 o[8];
+        float4 o[8][1];
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
           const bool there = i0 + i <= c1;
-          const float* p = part(there ? i0 + i : c1);
+          const float* p = a.part + (size_t)(2 * (i0 + i) + (i0 + i == c0 ? 1 : 0)) * SLOT;
           m[i] = there ? __ldcg(p + RB * D + row) : -INFINITY;
-          q[i] = __ldcg(p + RB * D + RB + row);
-          o[i] = __ldcg(reinterpret_cast<const float4*>(p + row * D + d));
+          q[i] = there ? __ldcg(p + RB * D + RB + row) : 0.f;
+          o[i][0] = there ? __ldcg(reinterpret_cast<const float4*>(p + row * D + d)) : zero4;
         }
         add_parts(m, q, o, &top, &l, y);
       }
-      result(s, row, d, top, l, y, nullptr);
+      result(s_chain[s_last[k]].s, row, d, 4, top, l, y, nullptr);
     }
   }
 }

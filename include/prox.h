@@ -401,8 +401,11 @@ PROX_API prox_status prox_linear4_destroy(prox_linear4* lin);
 /* out[b, n] = sum_g scales[g, n] sum_{k in g} q[k, n] x[b, k] for B tokens,
  * 1 <= B <= 16.  x: [B, d_in] and out: [B, d_out] of `dtype`, rows x_stride
  * and out_stride elements apart (at least d_in / d_out; out may not overlap
- * x).  fp16 and bf16 inputs enter the products exactly, fp32 inputs with 22
- * significant bits; sums are fp32.  A token with an infinity or NaN has
+ * x).  Inputs enter the products in fp16, scaled by a power of two per token and
+ * group of 128: fp16 and bf16 exactly down to 2^-25 of the group's largest
+ * magnitude, fp32 with 22 bits (two numbers).  A group's sum is good to 2^-16
+ * (fp32 inputs: 2^-20) of a code step of its largest input, the groups' sums are
+ * scaled and added in fp32.  A token with an infinity or NaN has
  * non-finite results; other tokens are not touched by it.  Results do not
  * depend on timing; no scratch is shared, so calls on one handle may overlap.
  * Allocates nothing and does not synchronise. */
@@ -462,8 +465,9 @@ PROX_API prox_status prox_kv4_read(const prox_kv4* cache, const int64_t* slots, 
  * Tq >= 1; cols * page_size * Tq * n_q_heads < 2^36; scale finite.  An entry outside [0, num_pages) sets
  * PROX_DEVERR_PAGE, a length outside [0, cols * page_size] PROX_DEVERR_LEN;
  * that request's result is then meaningless, and no memory outside the cache
- * is touched.  Scores, softmax statistics and sums are fp32; fp16 and bf16
- * queries enter the products exactly and probabilities with 11 bits, for fp32
+ * is touched.  Softmax statistics, outputs and the sums over rows are fp32; fp16
+ * and bf16 queries enter the products as they are, probabilities with 11 bits,
+ * and sums of up to 64 rows are good to 2^-14 of a code step; for fp32 queries
  * both carry 22.  Results do not depend on timing. */
 PROX_API prox_status prox_kv4_attend(const prox_kv4* cache, const void* q, int64_t q_req, int64_t q_tok,
                                      int64_t q_head, int n_q_heads, int B, int Tq, const int32_t* table,
