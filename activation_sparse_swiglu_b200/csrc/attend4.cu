@@ -29,7 +29,7 @@
 // columns.  bf16 and fp32 queries are scaled by a power of two.  (Exact
 // widening for all types, 32 rows a step and a page lookup per 16-byte copy
 // took 1080 instructions per 32 rows and 132 us for 64 requests of the
-// 8B-shaped model; it is 555 now and 80 us, the loop itself at 5 TB/s.)
+// 8B-shaped model; it is 555 now and 71 us, the loop itself at 5 TB/s.)
 // Probabilities times vs are scaled by a power of two per step so that they
 // use fp16's range; each step's product starts afresh and joins the fp32
 // output with one fused multiply-add, so the tensor core's own sums stay short.

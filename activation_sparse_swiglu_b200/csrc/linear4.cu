@@ -11,18 +11,21 @@
 // reads contiguously, and no shuffle or shared memory stands between HBM and
 // the tensor core.
 //
-// A code masked out of a word is an fp16 subnormal, n 2^-24 times its place, so
-// decoding takes logical instructions only; the other operand takes up the
-// places' factors, and the sum starts from -8 sum_k x, which makes n the code q.
-// (Widening to exact integers q takes 9 instructions for 8 codes; the 16-token
-// head then ran at 0.49 of the copy bandwidth, bound by issue.)
-// The tensor core aligns products by the exponents of their factors, which for
-// a subnormal is that of the largest one: a code n 2^-24 x has 2^-14 of a code
-// step of x left for rounding, 64 n 2^-24 x has 2^-20.  So the words hold their
-// codes where the mantissa's upper bits are (decode_words): fp32 inputs shift
-// every code there (7 instructions for 8 codes), 16-bit inputs leave half of
-// them 4 bits lower (5 instructions; 2^-16 of a code step, below the 2^-12 of
-// the result's own rounding).
+// 16-bit inputs: a code masked out of a word is an fp16 subnormal, n 2^-24 times
+// its place, so decoding takes 5 logical instructions for 8 codes; x takes up
+// the places' factors, and the sum starts from -8 sum_k x, which makes n the
+// code q.  (Widening to exact integers q takes 9; the 16-token head then ran at
+// 0.49 of the copy bandwidth.)  The tensor core aligns products by the exponents
+// of their factors, which for a subnormal is that of the largest one: a code
+// n 2^-24 x has 2^-14 of a code step of x left for rounding, 4 n 2^-24 x has
+// 2^-16, 64 n 2^-24 x 2^-20.  So the words hold their codes in the mantissa's
+// upper bits (decode_words): 2^-16 of a code step, below the 2^-12 of the
+// result's own rounding.
+// fp32 inputs: the same fields widened to exact integers q, 9 instructions for 8
+// codes, so that a group's large input does not take away from its small ones.
+// 4096 x 6144 at one token: 6.8 us and 1.2e-7 off.  (All codes at the highest
+// place, 7 logical instructions: 6.1 us and 4e-7, and a fixed 2^-20 of a code
+// step of the largest input even where that input's codes are 0.)
 //
 // x is held in fp16, scaled by a power of two per token and group of 128 that
 // brings the group's largest magnitude to 2^14: fp16 and bf16 values keep all
@@ -115,18 +118,22 @@ __device__ __forceinline__ int range_of(int U, int u, int W) {
 // A in bits 6-9, B in 2-5, C in 10-13, and D in 14-15 with its upper two bits
 // in bits 0-1 of the other half, so that a rotation by 8 brings D to 6-9 and C
 // to 2-5.  r: A fragments in the order a0 (B), a1 (C), a2 (A), a3 (D).
-// ALL_HIGH: every code at 6-9 (64 n 2^-24); else B and C at 2-5 (4 n 2^-24).
-template <bool ALL_HIGH>
+// EXACT: as integers q; else as subnormals, B and C at 2-5 (4 n 2^-24), A and D
+// at 6-9 (64 n 2^-24).
+template <bool EXACT>
 __device__ __forceinline__ void decode_words(uint32_t w, uint32_t (&r)[4]) {
   const uint32_t rot = __funnelshift_r(w, w, 8);
   r[2] = w & 0x03C003C0u;
   r[3] = rot & 0x03C003C0u;
-  if (ALL_HIGH) {
-    r[0] = (w << 4) & 0x03C003C0u;
-    r[1] = (w >> 4) & 0x03C003C0u;
-  } else {
-    r[0] = w & 0x003C003Cu;
-    r[1] = rot & 0x003C003Cu;
+  r[0] = w & 0x003C003Cu;
+  r[1] = rot & 0x003C003Cu;
+  if (EXACT) {
+    // in the mantissas of 256 and of 16: 256 + n and 16 + n
+    const __half2 low = bits_h2(0xDC20DC20u), high = bits_h2(0xCE00CE00u);  // -264, -24
+    r[2] = h2_bits(__hadd2(bits_h2(r[2] | 0x4C004C00u), high));
+    r[3] = h2_bits(__hadd2(bits_h2(r[3] | 0x4C004C00u), high));
+    r[0] = h2_bits(__hadd2(bits_h2(r[0] | 0x5C005C00u), low));
+    r[1] = h2_bits(__hadd2(bits_h2(r[1] | 0x5C005C00u), low));
   }
 }
 
@@ -164,10 +171,10 @@ __global__ void __launch_bounds__(warps_of(NT) * 32, 1) linear4_kernel(const Lin
   constexpr int PARTS = DT == PROX_F32 ? 2 : 1;
   constexpr int NC = 2 / PARTS;       // tokens of a thread per column tile
   constexpr int TB = 8 * NT / PARTS;  // tokens
-  constexpr bool ALL_HIGH = PARTS == 2;
-  constexpr float kStep = ALL_HIGH ? 0x1p-18f : 0x1p-22f;  // a code step in the products
+  constexpr bool EXACT = PARTS == 2;
+  constexpr float kStep = EXACT ? 1.f : 0x1p-22f;  // a code step in the products
   // x at input rows 2, 3 mod 4, whose codes stand at 6-9, against rows 0, 1
-  constexpr float kHigh = ALL_HIGH ? 1.f : 0.0625f;
+  constexpr float kHigh = EXACT ? 1.f : 0.0625f;
   extern __shared__ __align__(16) char smem[];
   __shared__ int2 s_cut[kWarps];  // of warps 0 .. W - 2; the last entry: a bit for each that is cut
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -334,10 +341,7 @@ __global__ void __launch_bounds__(warps_of(NT) * 32, 1) linear4_kernel(const Lin
           const float2 b0 = __half22float2(h0), b1 = __half22float2(h1);
           *reinterpret_cast<uint2*>(col + 8 * piece) = make_uint2(h2_bits(h0), h2_bits(h1));
           const __half2 l0 = __floats2half2_rn(y[0] - b0.x, y[1] - b0.y), l1 = __floats2half2_rn(y[2] - b1.x, y[3] - b1.y);
-          const float2 m0 = __half22float2(l0), m1 = __half22float2(l1);
           *reinterpret_cast<uint2*>(col + xs + 8 * piece) = make_uint2(h2_bits(l0), h2_bits(l1));
-          sum += (b0.x + m0.x) + (b0.y + m0.y);
-          sum = fmaf((b1.x + m1.x) + (b1.y + m1.y), 1.f / kHigh, sum);
         } else {
           *reinterpret_cast<uint4*>(col + 16 * piece) =
               make_uint4(scale2<DT>(raw[j].x, f, f, &sum), scale2<DT>(raw[j].y, f, f16, &sum),
@@ -345,8 +349,10 @@ __global__ void __launch_bounds__(warps_of(NT) * 32, 1) linear4_kernel(const Lin
         }
       }
       const unsigned mask = (LPG == 8 ? 0xFFu : 0xFu) << (lane / LPG * LPG);
+      if (!EXACT) {
 #pragma unroll
-      for (int o = LPG / 2; o > 0; o >>= 1) sum += __shfl_xor_sync(mask, sum, o);
+        for (int o = LPG / 2; o > 0; o >>= 1) sum += __shfl_xor_sync(mask, sum, o);
+      }
       if (lane % LPG == 0) s_nf[gr * TB + b] = make_float2(inv_pow2(f), -8.f * kStep * sum);
     }
     __syncthreads();
@@ -385,8 +391,7 @@ __global__ void __launch_bounds__(warps_of(NT) * 32, 1) linear4_kernel(const Lin
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
           if constexpr (PARTS == 2) {
-            const uint2 f = lds64(nf + 32 * n);
-            inv[n][0] = __uint_as_float(f.x), start[n][0] = __uint_as_float(f.y);
+            inv[n][0] = __uint_as_float(lds32(nf + 32 * n));
           } else {
             const uint4 f = lds128(nf + 64 * n);
             inv[n][0] = __uint_as_float(f.x), start[n][0] = __uint_as_float(f.y);
@@ -410,18 +415,17 @@ __global__ void __launch_bounds__(warps_of(NT) * 32, 1) linear4_kernel(const Lin
           for (int m = 0; m < 2; ++m) {
             const uint4 w4 = w[m][i >> 1];
             uint32_t r[4];
-            decode_words<ALL_HIGH>((i & 1) ? w4.z : w4.x, r);
+            decode_words<EXACT>((i & 1) ? w4.z : w4.x, r);
 #pragma unroll
             for (int n = 0; n < NT; ++n) {
               if (i == 0) {
-                // the lo columns of fp32 start from zero
-                const float c0 = start[n][0], c1 = PARTS == 2 ? 0.f : start[n][NC - 1];
+                const float c0 = EXACT ? 0.f : start[n][0], c1 = EXACT ? 0.f : start[n][NC - 1];
                 mma_f16(d[m][n], r[0], r[1], r[2], r[3], xv[n].x, xv[n].y, c0, c1, c0, c1);
               } else {
                 mma_f16(d[m][n], r[0], r[1], r[2], r[3], xv[n].x, xv[n].y);
               }
             }
-            decode_words<ALL_HIGH>((i & 1) ? w4.w : w4.y, r);
+            decode_words<EXACT>((i & 1) ? w4.w : w4.y, r);
 #pragma unroll
             for (int n = 0; n < NT; ++n) mma_f16(d[m][n], r[0], r[1], r[2], r[3], xv[n].z, xv[n].w);
           }

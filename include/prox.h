@@ -403,11 +403,11 @@ PROX_API prox_status prox_linear4_destroy(prox_linear4* lin);
  * and out_stride elements apart (at least d_in / d_out; out may not overlap
  * x).  Inputs enter the products in fp16, scaled by a power of two per token and
  * group of 128: fp16 and bf16 exactly down to 2^-25 of the group's largest
- * magnitude, fp32 with 22 bits (two numbers).  A group's sum is good to 2^-16
- * (fp32 inputs: 2^-20) of a code step of its largest input, the groups' sums are
- * scaled and added in fp32.  A token with an infinity or NaN has
- * non-finite results; other tokens are not touched by it.  Results do not
- * depend on timing; no scratch is shared, so calls on one handle may overlap.
+ * magnitude, fp32 with 22 bits (two numbers).  For 16-bit inputs a group's sum
+ * is good to 2^-16 of a code step of its largest input, for fp32 it is an fp32
+ * sum; the groups' sums are scaled and added in fp32.  A token with an infinity
+ * or NaN has non-finite results; other tokens are not touched by it.  Results do
+ * not depend on timing; no scratch is shared, so calls on one handle may overlap.
  * Allocates nothing and does not synchronise. */
 PROX_API prox_status prox_linear4_forward(const prox_linear4* lin, const void* x, int64_t x_stride, void* out,
                                           int64_t out_stride, int B, int dtype, void* stream);

@@ -37,22 +37,25 @@ def linear4(x, codes, scales):
     w = (q * s).view(K, N)
     xd = x.double()
     y = xd @ w
-    # The sums run over codes q + 8 and start from -8 sum x: terms of up to
-    # (|q| + 16) |x| S.  The groups' sums are added one after the other, after
-    # at most 8 tensor core steps and 3 multiplications; warps and CTAs join
-    # 16 + 8 parts; the start value is a sum of 128 values over 7 levels.
-    mag = xd.abs() @ ((q.abs() + 16) * s.abs()).view(K, N)
+    # For 16-bit inputs the sums run over codes q + 8 and start from -8 sum x:
+    # terms of up to (|q| + 16) |x| S.  The groups' sums are added one after the
+    # other, after at most 8 tensor core steps and 3 multiplications; warps and
+    # CTAs join 16 + 8 parts; the start value is a sum of 128 values over 7 levels.
+    wide = x.dtype == torch.float32
+    size = (q.abs() + (0 if wide else 16)) * s.abs()
+    mag = xd.abs() @ size.view(K, N)
     n = K // 128 + 8 + 3 + 24 + 7
     tol = n * 2.0 ** -23 * mag + HALF_STEP[x.dtype] * y.abs()
     # fp32 inputs carry 22 bits; what lies below 2^-25 of its group's largest
     # magnitude has an absolute step of 2^-38 of it (2^-39 off, hi and lo)
-    if x.dtype == torch.float32:
+    if wide:
         tol = tol + 2.0 ** -22 * mag
     top = xd.abs().view(-1, K // 128, 128).amax(-1)
-    tol = tol + 2.0 ** -38 * (top @ ((q.abs() + 16) * s.abs()).sum(1))
+    tol = tol + 2.0 ** -38 * (top @ size.sum(1))
     # the tensor core aligns subnormal codes at 2^-14: each of a group's 8 steps
-    # is off by up to 2^-16 (fp32 inputs 2^-20) of a code step of the largest x
-    tol = tol + 8 * 2.0 ** (-20 if x.dtype == torch.float32 else -16) * (top @ s.squeeze(1).abs())
+    # is off by up to 2^-16 of a code step of the largest x
+    if not wide:
+        tol = tol + 8 * 2.0 ** -16 * (top @ s.squeeze(1).abs())
     if x.dtype == torch.float16:
         tol = tol + 2.0 ** -24  # below fp16's normal range a step is 2^-24
     return y, tol

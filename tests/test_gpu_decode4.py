@@ -97,6 +97,16 @@ def test_linear4_wide_ranges(prox, dtype):
         within(y, want, tol + 2.0 ** -126)
 
 
+def test_linear4_large_input_at_zero_codes(prox):
+    """One input 10^4 times the others of its group, where every code is 0 (a
+    byte 0x88): an fp32 result is made of the others, and keeps their bits."""
+    codes, scales, x = linear_case(prox, 1024, 96, 3, torch.float32, seed=8)
+    x[:, 130] = 1e4
+    codes[130] = 0x88
+    want, tol = ref.linear4(x, codes, scales)
+    within(prox.Linear4(codes=codes, scales=scales)(x), want, tol)
+
+
 @pytest.mark.parametrize("dtype", ref.TYPES)
 def test_linear4_non_finite_token_stays_its_own(prox, dtype):
     codes, scales, x = linear_case(prox, 512, 64, 4, dtype, seed=11)
