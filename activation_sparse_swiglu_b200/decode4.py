@@ -34,12 +34,17 @@ def _raw_stream(stream, index: int) -> int:
     return stream.cuda_stream if isinstance(stream, torch.cuda.Stream) else int(stream)
 
 
+def on_stream(stream, device: torch.device):
+    """Context in which `stream` (a torch stream or a raw handle) is current."""
+    if not isinstance(stream, torch.cuda.Stream):
+        stream = torch.cuda.ExternalStream(int(stream), device=device)
+    return torch.cuda.stream(stream)
+
+
 def _empty(device: torch.device, shape, dtype, stream) -> torch.Tensor:
     """A result tensor that belongs to the stream that writes it."""
-    if isinstance(stream, torch.cuda.Stream):
-        with torch.cuda.stream(stream):
-            return torch.empty(shape, dtype=dtype, device=device)
-    return torch.empty(shape, dtype=dtype, device=device)
+    with on_stream(stream, device):
+        return torch.empty(shape, dtype=dtype, device=device)
 
 
 class Linear4:
@@ -279,15 +284,17 @@ class Attention4:
     def step(self, x: torch.Tensor, plan: PagePlan, table: torch.Tensor, stream=None) -> torch.Tensor:
         """x [B, d], one new token of each request (B <= 16), under a plan in
         which every request gains one -> [B, d]."""
+        if stream is not None:  # what the step makes on the way belongs to its stream
+            with on_stream(stream, self.qkv.device):
+                return self.step(x, plan, table)
         B, D = x.shape[0], self.head_dim
-        heads = self.qkv.forward(x, stream=stream).view(B, self.n_heads + 2 * self.n_kv_heads, D)
+        heads = self.qkv.forward(x).view(B, self.n_heads + 2 * self.n_kv_heads, D)
         q, k, v = heads.split_with_sizes([self.n_heads, self.n_kv_heads, self.n_kv_heads], 1)
         if self.rotate is not None:
-            with torch.cuda.stream(stream if isinstance(stream, torch.cuda.Stream) else None):
-                q, k = self.rotate(q, k, plan.positions[:B])
-        self.cache.append(k, v, plan.slots[:B], stream=stream)
-        o = self.cache.attend(q, table, plan.lens, stream=stream)
-        return self.out.forward(o.view(B, self.n_heads * D), stream=stream)
+            q, k = self.rotate(q, k, plan.positions[:B])
+        self.cache.append(k, v, plan.slots[:B])
+        o = self.cache.attend(q, table, plan.lens)
+        return self.out.forward(o.view(B, self.n_heads * D))
 
     def close(self):
         self.qkv.close()

@@ -14,6 +14,7 @@ import math
 import torch
 
 from . import MASK_THRESHOLD, MASK_TOPK, Layer, calibrate_thresholds, rmsnorm
+from .decode4 import on_stream
 
 ARTEFACT_FORMAT = "prox-thresholds"
 ARTEFACT_VERSION = 1
@@ -153,12 +154,14 @@ class Stack:
         layer's output [B, d]."""
         if self.attention is None:
             raise RuntimeError("the stack has no attention sub-layers")
+        if stream is not None:  # what the step makes on the way belongs to its stream
+            with on_stream(stream, x.device):
+                return self.decode(x, plan, table)
         y = None
         for li, (attn, layer) in enumerate(zip(self.attention, self.layers)):
             if li > 0:
-                x = rmsnorm(y, stream=stream)
-            a = attn.step(x, plan, table, stream=stream)
-            y = layer.forward(rmsnorm(a, stream=stream), stream=stream)
+                x = rmsnorm(y)
+            y = layer.forward(rmsnorm(attn.step(x, plan, table)))
         return y
 
     def close(self):

@@ -767,3 +767,39 @@ def test_stack_decodes_through_attention(prox):
         prox.Attention4(qkv[0], wo[0], 4, 3, D, num_pages=4)
     with pytest.raises(ValueError):
         prox.Attention4(qkv[0], qkv[0], Hq, Hkv, D, num_pages=4)
+
+
+@pytest.mark.parametrize("raw", [False, True])
+def test_decode_step_belongs_to_its_stream(prox, raw):
+    """stream= as a torch stream or a raw handle: rotate() runs on it, and the
+    tensors the step makes come from its memory, so that what the current
+    stream makes and fills meanwhile cannot be theirs."""
+    from activation_sparse_swiglu_b200.stack import Stack
+    d, F, H, D, B, page = 256, 512, 4, 64, 4, 16
+    g = gen_of(31)
+    w = lambda *s: (0.05 * torch.randn(s, device="cuda", generator=g)).to(torch.bfloat16)  # noqa: E731
+    ffn, qkv, wo = [(w(d, F), w(d, F), w(F, d))], w(d, 3 * H * D), w(H * D, d)
+    seen = []
+
+    def rotate(q, k, positions):
+        seen.append(torch.cuda.current_stream().cuda_stream)
+        return q * 1.5, k * 0.5
+
+    def run(stream):
+        attn = prox.Attention4(qkv, wo, H, H, D, num_pages=4, page_size=page, rotate=rotate)
+        stack = Stack(ffn, k=F, max_batch=B, attention=[attn])
+        table = torch.arange(B, dtype=torch.int32, device="cuda").view(B, 1)
+        ones = torch.ones(B, dtype=torch.int32, device="cuda")
+        plan = prox.PagePlan(ones, None, None, torch.arange(B, device="cuda") * page, ones - 1, None)
+        x = torch.randn((B, d), device="cuda", generator=gen_of(32))
+        torch.cuda.synchronize()
+        y = stack.decode(x, plan, table, stream=stream)
+        trash = [torch.full((B, n), 7.0, device="cuda") for n in (d, d, d, H * D, 3 * H * D)]
+        torch.cuda.synchronize()
+        del trash
+        return y
+
+    side = torch.cuda.Stream()
+    want = run(None)
+    assert torch.equal(run(side.cuda_stream if raw else side), want)
+    assert seen == [torch.cuda.current_stream().cuda_stream, side.cuda_stream]
