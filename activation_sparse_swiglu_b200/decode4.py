@@ -204,7 +204,7 @@ class KVCache4:
         if self._h is None:
             raise RuntimeError("the cache is closed")
         kv = None
-        if stream is not None:
+        if stream is not None and isinstance(slots, torch.Tensor) and slots.is_cuda:
             shape = (slots.numel(), self.n_heads, self.head_dim)
             kv = tuple(_empty(self.device, shape, dtype, stream) for _ in range(2))
             stream = _raw_stream(stream, self._index)
@@ -248,7 +248,7 @@ def plan_pages(lens: torch.Tensor, delta: torch.Tensor, table: torch.Tensor, fre
     free_count are updated in place too (and returned); otherwise the new ones
     are new tensors and the same plan may be made again."""
     made = None
-    if stream is not None:
+    if stream is not None and isinstance(lens, torch.Tensor) and lens.is_cuda:
         made = (_empty(lens.device, (2 * lens.numel() + 3 + max(0, max_new),), torch.int32, stream),
                 _empty(lens.device, (max(0, max_new),), torch.int64, stream))
         stream = _raw_stream(stream, lens.device.index)

@@ -97,3 +97,6 @@ def test_binding_refuses_host_tensors_and_wrong_types():
     i = torch.zeros(4, dtype=torch.int32)
     with pytest.raises(TypeError, match="lens"):
         prox.plan_pages(i, i, torch.zeros(4, 8, dtype=torch.int32), i, i[:1], 64, max_new=4)
+    for lens in (i, [0]):  # refused as without a stream
+        with pytest.raises(TypeError, match="lens"):
+            prox.plan_pages(lens, i, torch.zeros(4, 8, dtype=torch.int32), i, i[:1], 64, max_new=4, stream=1)
