@@ -37,7 +37,13 @@ def _raw_stream(stream, index: int) -> int:
 def on_stream(stream, device: torch.device):
     """Context in which `stream` (a torch stream or a raw handle) is current."""
     if not isinstance(stream, torch.cuda.Stream):
-        stream = torch.cuda.ExternalStream(int(stream), device=device)
+        # 0 and 1 (cudaStreamLegacy) are handles of the default stream.  As an
+        # ExternalStream torch would take 0 for "none given" and make one of its
+        # pool, which nothing orders behind the caller's work, and 1 (its own
+        # streams have odd ids) for one of its own.
+        handle = int(stream)
+        stream = (torch.cuda.default_stream(device) if handle in (0, 1)
+                  else torch.cuda.ExternalStream(handle, device=device))
     return torch.cuda.stream(stream)
 
 
