@@ -13,6 +13,7 @@ namespace prox {
 constexpr int kGroupRows = 128;  // input rows of one weight scale
 constexpr int kLinear4MaxTokens = 16;
 constexpr int kPlanMaxRequests = 8192;    // bounds the page plan's shared memory
+constexpr int kPlanMaxNew = 1 << 30;      // token numbers plus a grid's stride stay in 32 bits
 constexpr int kAttendMaxRequests = 8192;  // bounds the attention's table of chunk counts
 
 }  // namespace prox

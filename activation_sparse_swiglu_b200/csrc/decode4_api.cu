@@ -325,6 +325,7 @@ prox_status prox_plan_pages(const int32_t* lens, const int32_t* delta, int B, in
   if (cols < 0 || table_stride < cols || (int64_t)B * cols > INT_MAX)
     return fail(PROX_EINVAL, "cols=%d must be >= 0, table_stride >= cols and B * cols < 2^31", cols);
   if (free_cap < 0 || max_new < 0) return fail(PROX_EINVAL, "free_cap and max_new must be >= 0");
+  if (max_new > prox::kPlanMaxNew) return fail(PROX_EINVAL, "max_new=%d must be at most 2^30", max_new);
   const void* words[] = {lens, delta, free_count, lens_out, free_count_out, cu, status};
   for (const void* w : words)
     if (!w || !aligned4(w)) return fail(PROX_EINVAL, "pointers must be non-NULL and 4-byte aligned");

@@ -140,7 +140,9 @@ __global__ void __launch_bounds__(1024, 1) page_plan_kernel(PagePlan p, int ctas
     return j < c0 ? p.free_pages[j] : returned_page((int)(j - c0));
   };
   if (!bad) {
-    for (int n = at; n < max(returned, taken); n += all) {  // both lookups before either write
+    const unsigned moved = max(returned, taken);  // (up to 2^31: n may pass it by the CTAs' threads)
+    for (unsigned u = at; u < moved; u += all) {  // both lookups before either write
+      const int n = (int)u;
       const int back = n < returned ? returned_page(n) : 0;
       if (n < taken) {
         const int i = find_row(s_gain, p.B, n), id = taken_page(n);
@@ -156,7 +158,7 @@ __global__ void __launch_bounds__(1024, 1) page_plan_kernel(PagePlan p, int ctas
     __syncthreads();
   const int lane = tid & 31;
   const bool sparse = total < 4 * p.B;  // few tokens a request: a search each beats the steps
-  const int per_lane = p.max_new <= all ? 1 : 4;
+  const int per_lane = p.max_new <= all ? 1 : 4;  // (n0 stays below kPlanMaxNew + 4 all)
   for (int n0 = (at >> 5) * (32 * per_lane); n0 < p.max_new; n0 += all * per_lane) {
     int i = !sparse && n0 < total ? find_row(s_new, p.B, n0) : 0;
     int pos[4], id[4];

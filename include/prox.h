@@ -493,7 +493,8 @@ PROX_API prox_status prox_kv4_attend(const prox_kv4* cache, const void* q, int64
  * (free_cap entries).  lens_out may be lens, and free_count_out free_count (a
  * plan that is committed at once); otherwise the same plan may be made again.
  * Freed table entries keep their values.  1 <= B <= 8192, 1 <= page_size <= 2^30,
- * cols >= 0, B * cols < 2^31; all int32 unless said; device pointers. */
+ * cols >= 0, B * cols < 2^31, 0 <= max_new <= 2^30; all int32 unless said; device
+ * pointers. */
 PROX_API prox_status prox_plan_pages(const int32_t* lens, const int32_t* delta, int B, int page_size, int32_t* table,
                                      int64_t table_stride, int cols, int32_t* free_pages, int free_cap,
                                      const int32_t* free_count, int32_t* lens_out, int32_t* free_count_out,
