@@ -187,7 +187,7 @@ __global__ void __launch_bounds__(warps_of(D, NT, parts_of(DT)) * 32, 1) attend4
     pre[i] = (int)at;
     at += kStartUnits + max(1, (min(max(c.lens[i], 0), max_len) + kUnit - 1) / kUnit);
   }
-  if (threadIdx.x == 0) pre[c.B] = (int)total;
+  if (threadIdx.x == 0) pre[c.B] = (int)total;  // (the host has seen that B full tables stay below 2^31)
   if (threadIdx.x < kMaxWarps) s_head_at[threadIdx.x] = s_tail_at[threadIdx.x] = 0;
   if (threadIdx.x == 0) s_chains = 0;
   __syncthreads();
@@ -231,8 +231,8 @@ __global__ void __launch_bounds__(warps_of(D, NT, parts_of(DT)) * 32, 1) attend4
   long long cb, wb, we;
   {
     const long long all = (long long)H * (total - (long long)kStartUnits * c.B);  // units
-    const unsigned span = (unsigned)(cta1 - cta0);  // (H 2^27 / P at most, times 12)
-    const long long place = lane == 0 ? cta0 : cta0 + (long long)span * (warp + (lane == 2)) / warps;
+    const long long span = cta1 - cta0;  // (places are below 2^31 units times 2^20 row blocks)
+    const long long place = lane == 0 ? cta0 : cta0 + span * (warp + (lane == 2)) / warps;
     Cursor s = seek(place < places ? place : places - 1);
     const long long u = place < places ? s.beg + s.c : all;
     cb = __shfl_sync(0xffffffffu, u, 0);

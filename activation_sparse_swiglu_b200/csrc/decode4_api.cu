@@ -288,6 +288,9 @@ prox_status prox_kv4_attend(const prox_kv4* C, const void* q, int64_t q_req, int
   if (cols < 0 || table_stride < cols) return fail(PROX_EINVAL, "cols=%d must be >= 0 and table_stride >= cols", cols);
   if (((int64_t)cols * C->page / 32 + 3) * Tq * n_q_heads >= (int64_t)1 << 32)
     return fail(PROX_EINVAL, "cols * page_size * Tq * n_q_heads must stay below 2^36");
+  // (units of 32 rows, 2 for a start and 1 for a ragged end, of all requests: see attend4.cu)
+  if (((int64_t)cols * C->page / 32 + 3) * B > INT_MAX)
+    return fail(PROX_EINVAL, "B * cols * page_size must stay below 2^36 (with 96 tokens more a request)");
   if (!std::isfinite(scale)) return fail(PROX_EINVAL, "scale must be finite");
   if (!q || !aligned(q, dtype_size(dtype)) || !out || !aligned16(out))
     return fail(PROX_EINVAL, "q must be aligned to its type and out a 16-byte aligned pointer");

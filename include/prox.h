@@ -462,7 +462,8 @@ PROX_API prox_status prox_kv4_read(const prox_kv4* cache, const int64_t* slots, 
  * type; lse (may be NULL): fp32 [B, Tq, n_q_heads], log sum_j exp(scale q.K_j).
  * table: int32 [B, cols], rows table_stride apart; entries behind a request's
  * last page are not read.  n_q_heads a multiple of n_heads; 1 <= B <= 8192;
- * Tq >= 1; cols * page_size * Tq * n_q_heads < 2^36; scale finite.  An entry outside [0, num_pages) sets
+ * Tq >= 1; cols * page_size * Tq * n_q_heads < 2^36; B * (cols * page_size + 96)
+ * < 2^36; scale finite.  An entry outside [0, num_pages) sets
  * PROX_DEVERR_PAGE, a length outside [0, cols * page_size] PROX_DEVERR_LEN;
  * that request's result is then meaningless, and no memory outside the cache
  * is touched.  Softmax statistics, outputs and the sums over rows are fp32; fp16
