@@ -49,6 +49,36 @@ bool rows_overlap(const void* a, int64_t n_a, int64_t s_a, const void* b, int64_
   return d < n_a * size || d + n_b * size > stride;
 }
 
+struct Span {
+  uintptr_t lo, hi;
+  bool meets(const Span& o) const { return lo < o.hi && o.lo < hi; }
+};
+Span span_of(const void* p, int64_t n, size_t size) {
+  const uintptr_t at = reinterpret_cast<uintptr_t>(p);
+  return {at, at + n * size};
+}
+
+// Whether `w` meets the queries of any request.  (Between requests there may
+// be anything: q may be a column range of wider rows.)
+bool meets_queries(const Span& w, const prox::Attend4Call& c, int D) {
+  const size_t size = dtype_size(c.dtype);
+  auto queries = [&](int b0, int b1) {  // of requests [b0, b1]
+    int64_t lo = 0, hi = D;
+    auto along = [&](int64_t stride, int64_t first, int64_t last) {
+      lo += stride < 0 ? stride * last : stride * first;
+      hi += stride < 0 ? stride * first : stride * last;
+    };
+    along(c.q_req, b0, b1);
+    along(c.q_tok, 0, c.Tq - 1);
+    along(c.q_head, 0, c.Hq - 1);
+    return span_of(static_cast<const char*>(c.q) + lo * (int64_t)size, hi - lo, size);
+  };
+  if (!w.meets(queries(0, c.B - 1))) return false;
+  for (int b = 0; b < c.B; ++b)
+    if (w.meets(queries(b, b))) return true;
+  return false;
+}
+
 // Allocates the handle and its buffers for a checked shape.
 prox_status linear4_new(int d_in, int d_out, prox_linear4** out) {
   int dev, sms;
@@ -296,8 +326,6 @@ prox_status prox_kv4_attend(const prox_kv4* C, const void* q, int64_t q_req, int
     return fail(PROX_EINVAL, "q must be aligned to its type and out a 16-byte aligned pointer");
   if (!lens || !aligned4(lens) || (cols > 0 && (!table || !aligned4(table))) || !aligned4(lse))
     return fail(PROX_EINVAL, "lens, table and lse must be 4-byte aligned pointers");
-  prox_status st = on_device(C->device, "kv4 cache");
-  if (st != PROX_OK) return st;
   prox::Attend4Call c;
   c.q = q;
   c.q_req = q_req;
@@ -314,6 +342,21 @@ prox_status prox_kv4_attend(const prox_kv4* C, const void* q, int64_t q_req, int
   c.Hq = n_q_heads;
   c.dtype = dtype;
   c.scale = scale;
+  // A request's queries are read when its turn comes, other requests' results
+  // are written by then.  Results in the queries' own places are fine: a row is
+  // written after all that read it.
+  const int64_t rows = (int64_t)B * Tq * n_q_heads;
+  const Span to = span_of(out, rows * C->D, dtype_size(dtype)), lse_to = span_of(lse, lse ? rows : 0, 4);
+  const Span in_lens = span_of(lens, B, 4), in_table = span_of(table, cols ? (B - 1) * table_stride + cols : 0, 4);
+  const bool in_place = out == q && (n_q_heads == 1 || q_head == C->D) &&
+                        (Tq == 1 || q_tok == (int64_t)n_q_heads * C->D) &&
+                        (B == 1 || q_req == (int64_t)Tq * n_q_heads * C->D);
+  if ((!in_place && meets_queries(to, c, C->D)) || (lse && meets_queries(lse_to, c, C->D)))
+    return fail(PROX_EINVAL, "out and lse may not overlap q (unless out is q, contiguous)");
+  if (to.meets(lse_to) || to.meets(in_lens) || to.meets(in_table) || lse_to.meets(in_lens) || lse_to.meets(in_table))
+    return fail(PROX_EINVAL, "out and lse may not overlap each other, lens or table");
+  prox_status st = on_device(C->device, "kv4 cache");
+  if (st != PROX_OK) return st;
   PROX_CUDA(prox::launch_attend4(C, c, as_stream(stream)), "prox_kv4_attend launch");
   return PROX_OK;
 }

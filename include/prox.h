@@ -460,6 +460,8 @@ PROX_API prox_status prox_kv4_read(const prox_kv4* cache, const int64_t* slots, 
  * q: [B, Tq, n_q_heads, head_dim] of `dtype` with the given strides (elements;
  * the last dimension contiguous); out: contiguous, 16-byte aligned, the same
  * type; lse (may be NULL): fp32 [B, Tq, n_q_heads], log sum_j exp(scale q.K_j).
+ * out may be q itself where q is contiguous; else out and lse may overlap neither
+ * q, lens and table nor each other.
  * table: int32 [B, cols], rows table_stride apart; entries behind a request's
  * last page are not read.  n_q_heads a multiple of n_heads; 1 <= B <= 8192;
  * Tq >= 1; cols * page_size * Tq * n_q_heads < 2^36; B * (cols * page_size + 96)
