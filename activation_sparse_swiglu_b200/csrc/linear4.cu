@@ -11,21 +11,15 @@
 // reads contiguously, and no shuffle or shared memory stands between HBM and
 // the tensor core.
 //
-// 16-bit inputs: a code masked out of a word is an fp16 subnormal, n 2^-24 times
-// its place, so decoding takes 5 logical instructions for 8 codes; x takes up
-// the places' factors, and the sum starts from -8 sum_k x, which makes n the
-// code q.  (Widening to exact integers q takes 9; the 16-token head then ran at
-// 0.49 of the copy bandwidth.)  The tensor core aligns products by the exponents
-// of their factors, which for a subnormal is that of the largest one: a code
-// n 2^-24 x has 2^-14 of a code step of x left for rounding, 4 n 2^-24 x has
-// 2^-16, 64 n 2^-24 x 2^-20.  So the words hold their codes in the mantissa's
-// upper bits (decode_words): 2^-16 of a code step, below the 2^-12 of the
-// result's own rounding.
-// fp32 inputs: the same fields widened to exact integers q, 9 instructions for 8
-// codes, so that a group's large input does not take away from its small ones.
-// 4096 x 6144 at one token: 6.8 us and 1.2e-7 off.  (All codes at the highest
-// place, 7 logical instructions: 6.1 us and 4e-7, and a fixed 2^-20 of a code
-// step of the largest input even where that input's codes are 0.)
+// Codes are widened to exact fp16 integers q, 9 instructions for 8 of them
+// (decode_words), so that every product is exact and a sum is as good as the
+// tensor core's fp32, whatever the inputs' spread.  (For 16-bit inputs a code
+// masked out of its word, an fp16 subnormal, would do with 5: but the tensor
+// core aligns products by the exponents of their factors, a subnormal's being
+// that of the largest one, so an input 10^4 times the others took the others'
+// last bits even where its own codes are 0, by percents of a group's sum.  With
+// subnormals 28672 x 8192 takes 26.6 us for 5 tokens, 5120 x 131072 76.5 for 16;
+// with integers 28.8 and 82.6.)
 //
 // x is held in fp16, scaled by a power of two per token and group of 128 that
 // brings the group's largest magnitude to 2^14: fp16 and bf16 values keep all
@@ -117,24 +111,23 @@ __device__ __forceinline__ int range_of(int U, int u, int W) {
 // A word holds eight codes, two of each of four fields (one per 16-bit half):
 // A in bits 6-9, B in 2-5, C in 10-13, and D in 14-15 with its upper two bits
 // in bits 0-1 of the other half, so that a rotation by 8 brings D to 6-9 and C
-// to 2-5.  r: A fragments in the order a0 (B), a1 (C), a2 (A), a3 (D).
-// EXACT: as integers q; else as subnormals, B and C at 2-5 (4 n 2^-24), A and D
-// at 6-9 (64 n 2^-24).
-template <bool EXACT>
+// to 2-5.  r: A fragments in the order a0 (B), a1 (C), a2 (A), a3 (D), as
+// integers q: in the mantissas of 256 and of 16 the fields are 256 + n and
+// 16 + n.
+// (w & mask) | bits, as one instruction (left to the compiler it became two:
+// 34.6 us for 28672 x 8192 at 5 tokens instead of 28.8).
+__device__ __forceinline__ uint32_t and_or(uint32_t w, uint32_t mask, uint32_t bits) {
+  uint32_t r;
+  asm("lop3.b32 %0, %1, %2, %3, 0xEA;" : "=r"(r) : "r"(w), "r"(mask), "r"(bits));
+  return r;
+}
 __device__ __forceinline__ void decode_words(uint32_t w, uint32_t (&r)[4]) {
   const uint32_t rot = __funnelshift_r(w, w, 8);
-  r[2] = w & 0x03C003C0u;
-  r[3] = rot & 0x03C003C0u;
-  r[0] = w & 0x003C003Cu;
-  r[1] = rot & 0x003C003Cu;
-  if (EXACT) {
-    // in the mantissas of 256 and of 16: 256 + n and 16 + n
-    const __half2 low = bits_h2(0xDC20DC20u), high = bits_h2(0xCE00CE00u);  // -264, -24
-    r[2] = h2_bits(__hadd2(bits_h2(r[2] | 0x4C004C00u), high));
-    r[3] = h2_bits(__hadd2(bits_h2(r[3] | 0x4C004C00u), high));
-    r[0] = h2_bits(__hadd2(bits_h2(r[0] | 0x5C005C00u), low));
-    r[1] = h2_bits(__hadd2(bits_h2(r[1] | 0x5C005C00u), low));
-  }
+  const __half2 low = bits_h2(0xDC20DC20u), high = bits_h2(0xCE00CE00u);  // -264, -24
+  r[2] = h2_bits(__hadd2(bits_h2(and_or(w, 0x03C003C0u, 0x4C004C00u)), high));
+  r[3] = h2_bits(__hadd2(bits_h2(and_or(rot, 0x03C003C0u, 0x4C004C00u)), high));
+  r[0] = h2_bits(__hadd2(bits_h2(and_or(w, 0x003C003Cu, 0x5C005C00u)), low));
+  r[1] = h2_bits(__hadd2(bits_h2(and_or(rot, 0x003C003Cu, 0x5C005C00u)), low));
 }
 
 // The largest magnitude of 16 bytes of activations.
@@ -153,13 +146,11 @@ __device__ __forceinline__ float top(const uint4& u) {
                  fmaxf(fabsf(__uint_as_float(u.z)), fabsf(__uint_as_float(u.w))));
   }
 }
-// Two fp16 or bf16 values times a power of two `to`, as fp16 (exact above 2^-14);
-// adds them times f to *sum.
+// Two fp16 or bf16 values times a power of two f, as fp16 (exact above 2^-14).
 template <int DT>
-__device__ __forceinline__ uint32_t scale2(uint32_t w, float f, float to, float* sum) {
+__device__ __forceinline__ uint32_t scale2(uint32_t w, float f) {
   const float2 v = DT == PROX_F16 ? __half22float2(bits_h2(w)) : bf16x2_to_f2(w);
-  *sum = fmaf(v.x, f, fmaf(v.y, f, *sum));
-  return h2_bits(__floats2half2_rn(v.x * to, v.y * to));
+  return h2_bits(__floats2half2_rn(v.x * f, v.y * f));
 }
 
 // NT column tiles of 8 (tokens, or their hi / lo parts), PF units in flight
@@ -171,10 +162,6 @@ __global__ void __launch_bounds__(warps_of(NT) * 32, 1) linear4_kernel(const Lin
   constexpr int PARTS = DT == PROX_F32 ? 2 : 1;
   constexpr int NC = 2 / PARTS;       // tokens of a thread per column tile
   constexpr int TB = 8 * NT / PARTS;  // tokens
-  constexpr bool EXACT = PARTS == 2;
-  constexpr float kStep = EXACT ? 1.f : 0x1p-22f;  // a code step in the products
-  // x at input rows 2, 3 mod 4, whose codes stand at 6-9, against rows 0, 1
-  constexpr float kHigh = EXACT ? 1.f : 0.0625f;
   extern __shared__ __align__(16) char smem[];
   __shared__ int2 s_cut[kWarps];  // of warps 0 .. W - 2; the last entry: a bit for each that is cut
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -186,8 +173,7 @@ __global__ void __launch_bounds__(warps_of(NT) * 32, 1) linear4_kernel(const Lin
   const int cols = a.B * PARTS;
   const int xs = a.per_phase * 256 + kXPad;  // bytes of a column
   char* s_x = smem;
-  // per group and token: 1 / the power of two, and the sum's start value
-  float2* s_nf = reinterpret_cast<float2*>(smem + (size_t)cols * xs);        // [per_phase][TB]
+  float* s_nf = reinterpret_cast<float*>(smem + (size_t)cols * xs);          // [per_phase][TB] 1 / the powers of two
   float* s_res = reinterpret_cast<float*>(s_nf + a.per_phase * TB);          // [per_clus][B][kPartRow]
   // the warp's ring of PF units: this lane's 16 bytes of each row of codes, and
   // its scales
@@ -328,15 +314,14 @@ __global__ void __launch_bounds__(warps_of(NT) * 32, 1) linear4_kernel(const Lin
 #pragma unroll
       for (int o = LPG / 2; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
       if (gr >= nG) continue;
-      const float f = normaliser(mx), f16 = kHigh * f;
-      float sum = 0.f;  // of the group's x as the products will see it
+      const float f = normaliser(mx);
       char* col = s_x + (size_t)(b * PARTS) * xs + gr * 256 + (lane % LPG) * (DT == PROX_F32 ? 32 : 64);
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
         const int piece = (j + turn) & 3;
         if constexpr (DT == PROX_F32) {
           const float y[4] = {__uint_as_float(raw[j].x) * f, __uint_as_float(raw[j].y) * f,
-                              __uint_as_float(raw[j].z) * f16, __uint_as_float(raw[j].w) * f16};
+                              __uint_as_float(raw[j].z) * f, __uint_as_float(raw[j].w) * f};
           const __half2 h0 = __floats2half2_rn(y[0], y[1]), h1 = __floats2half2_rn(y[2], y[3]);
           const float2 b0 = __half22float2(h0), b1 = __half22float2(h1);
           *reinterpret_cast<uint2*>(col + 8 * piece) = make_uint2(h2_bits(h0), h2_bits(h1));
@@ -344,16 +329,11 @@ __global__ void __launch_bounds__(warps_of(NT) * 32, 1) linear4_kernel(const Lin
           *reinterpret_cast<uint2*>(col + xs + 8 * piece) = make_uint2(h2_bits(l0), h2_bits(l1));
         } else {
           *reinterpret_cast<uint4*>(col + 16 * piece) =
-              make_uint4(scale2<DT>(raw[j].x, f, f, &sum), scale2<DT>(raw[j].y, f, f16, &sum),
-                         scale2<DT>(raw[j].z, f, f, &sum), scale2<DT>(raw[j].w, f, f16, &sum));
+              make_uint4(scale2<DT>(raw[j].x, f), scale2<DT>(raw[j].y, f), scale2<DT>(raw[j].z, f),
+                         scale2<DT>(raw[j].w, f));
         }
       }
-      const unsigned mask = (LPG == 8 ? 0xFFu : 0xFu) << (lane / LPG * LPG);
-      if (!EXACT) {
-#pragma unroll
-        for (int o = LPG / 2; o > 0; o >>= 1) sum += __shfl_xor_sync(mask, sum, o);
-      }
-      if (lane % LPG == 0) s_nf[gr * TB + b] = make_float2(inv_pow2(f), -8.f * kStep * sum);
+      if (lane % LPG == 0) s_nf[gr * TB + b] = inv_pow2(f);
     }
     __syncthreads();
 
@@ -376,7 +356,7 @@ __global__ void __launch_bounds__(warps_of(NT) * 32, 1) linear4_kernel(const Lin
           for (int r = 0; r < 2; ++r)
 #pragma unroll
             for (int e = 0; e < NC; ++e) acc[m][n][r][e] = 0.f;
-      uint32_t xa[NT], nf = nf0 + gr0 * (TB * 8);
+      uint32_t xa[NT], nf = nf0 + gr0 * (TB * 4);
 #pragma unroll
       for (int n = 0; n < NT; ++n) xa[n] = xcol[n] + gr0 * 256;
       for (int i_unit = 0; i_unit < n_units; ++i_unit) {
@@ -387,15 +367,14 @@ __global__ void __launch_bounds__(warps_of(NT) * 32, 1) linear4_kernel(const Lin
 #pragma unroll
           for (int h = 0; h < 2; ++h) w[m][h] = lds128(slot + (2 * m + h) * 512);
         const uint2 scw = lds64(slot - lane * 8 + kCodeBytes);
-        float inv[NT][NC], start[NT][NC];
+        float inv[NT][NC];
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
           if constexpr (PARTS == 2) {
-            inv[n][0] = __uint_as_float(lds32(nf + 32 * n));
+            inv[n][0] = __uint_as_float(lds32(nf + 16 * n));
           } else {
-            const uint4 f = lds128(nf + 64 * n);
-            inv[n][0] = __uint_as_float(f.x), start[n][0] = __uint_as_float(f.y);
-            inv[n][NC - 1] = __uint_as_float(f.z), start[n][NC - 1] = __uint_as_float(f.w);
+            const uint2 f = lds64(nf + 32 * n);
+            inv[n][0] = __uint_as_float(f.x), inv[n][NC - 1] = __uint_as_float(f.y);
           }
         }
         // the copy into the slot just read starts once the reads (which come
@@ -415,17 +394,15 @@ __global__ void __launch_bounds__(warps_of(NT) * 32, 1) linear4_kernel(const Lin
           for (int m = 0; m < 2; ++m) {
             const uint4 w4 = w[m][i >> 1];
             uint32_t r[4];
-            decode_words<EXACT>((i & 1) ? w4.z : w4.x, r);
+            decode_words((i & 1) ? w4.z : w4.x, r);
 #pragma unroll
             for (int n = 0; n < NT; ++n) {
-              if (i == 0) {
-                const float c0 = EXACT ? 0.f : start[n][0], c1 = EXACT ? 0.f : start[n][NC - 1];
-                mma_f16(d[m][n], r[0], r[1], r[2], r[3], xv[n].x, xv[n].y, c0, c1, c0, c1);
-              } else {
+              if (i == 0)
+                mma_f16(d[m][n], r[0], r[1], r[2], r[3], xv[n].x, xv[n].y, 0.f, 0.f, 0.f, 0.f);
+              else
                 mma_f16(d[m][n], r[0], r[1], r[2], r[3], xv[n].x, xv[n].y);
-              }
             }
-            decode_words<EXACT>((i & 1) ? w4.w : w4.y, r);
+            decode_words((i & 1) ? w4.w : w4.y, r);
 #pragma unroll
             for (int n = 0; n < NT; ++n) mma_f16(d[m][n], r[0], r[1], r[2], r[3], xv[n].z, xv[n].w);
           }
@@ -433,7 +410,7 @@ __global__ void __launch_bounds__(warps_of(NT) * 32, 1) linear4_kernel(const Lin
 #pragma unroll
         for (int m = 0; m < 2; ++m) {
           const float2 s2 = __half22float2(bits_h2(m ? scw.y : scw.x));
-          const float s[2] = {s2.x * (1.f / kStep), s2.y * (1.f / kStep)};
+          const float s[2] = {s2.x, s2.y};
 #pragma unroll
           for (int n = 0; n < NT; ++n)
 #pragma unroll
@@ -446,7 +423,7 @@ __global__ void __launch_bounds__(warps_of(NT) * 32, 1) linear4_kernel(const Lin
         }
 #pragma unroll
         for (int n = 0; n < NT; ++n) xa[n] += 256;
-        nf += TB * 8;
+        nf += TB * 4;
       }
       // the strip's results, or this warp's part of them
       if (n_units == nG) {
@@ -618,7 +595,7 @@ bool plan_linear4(const prox_linear4* L, int strips, int B, int dtype, Plan* bes
     p.per_phase = p.per_rank;
     auto front = [&] {  // everything before the rings
       const int res = c > 1 || p.per_phase < p.per_rank ? p.per_clus : 0;
-      return ((size_t)cols * (p.per_phase * 256 + kXPad) + (size_t)p.per_phase * tb * 8 +
+      return ((size_t)cols * (p.per_phase * 256 + kXPad) + (size_t)p.per_phase * tb * 4 +
               (size_t)res * kPartRow * B * 4 + 15) & ~(size_t)15;
     };
     while (front() + ring_bytes(nt, 2) > kSmemLimit && p.per_phase > 1) p.per_phase = (p.per_phase + 1) / 2;

@@ -403,9 +403,8 @@ PROX_API prox_status prox_linear4_destroy(prox_linear4* lin);
  * and out_stride elements apart (at least d_in / d_out; out may not overlap
  * x).  Inputs enter the products in fp16, scaled by a power of two per token and
  * group of 128: fp16 and bf16 exactly down to 2^-25 of the group's largest
- * magnitude, fp32 with 22 bits (two numbers).  For 16-bit inputs a group's sum
- * is good to 2^-16 of a code step of its largest input, for fp32 it is an fp32
- * sum; the groups' sums are scaled and added in fp32.  A token with an infinity
+ * magnitude, fp32 with 22 bits (two numbers).  A group's sum is an fp32 sum of
+ * exact products; the groups' sums are scaled and added in fp32.  A token with an infinity
  * or NaN has non-finite results; other tokens are not touched by it.  Results do
  * not depend on timing; no scratch is shared, so calls on one handle may overlap.
  * Allocates nothing and does not synchronise. */
