@@ -18,21 +18,19 @@
 // conflict at head_dim 128 and 256 (see token_of).
 //
 // The kernel is bound by issue before it is by HBM unless decoding is cheap.
-// fp16 and bf16 queries: a nibble masked out of a word is an fp16 subnormal
-// (spread8), 5/8 of an instruction per code; the offset 8 is taken off in the
-// sums' start values: -8 sum_d Q_d for a score, and -8 sum_j p_j for an output,
-// which one product with a constant gives in the right registers.  Such
-// sums are then good to 2^-14 of a code step of the largest factor (see
-// spread8), a quarter of what rounding a probability to 11 bits costs.  fp32
-// queries are held to fp32: their codes are widened to exact
-// integers (9/8 instructions), queries and probabilities split into hi + lo
-// columns.  bf16 and fp32 queries are scaled by a power of two.  (Exact
-// widening for all types, 32 rows a step and a page lookup per 16-byte copy
-// took 1080 instructions per 32 rows and 132 us for 64 requests of the
-// 8B-shaped model; it is 555 now and 71 us, the loop itself at 5 TB/s.)
+// Codes are widened to exact fp16 integers (widen8, 9/8 of an instruction per
+// code), so products are exact and sums are fp32.  (A nibble masked out of a
+// word is an fp16 subnormal, 5/8 of an instruction; but the tensor core aligns
+// products by their factors' exponents, so a large query element or a heavy row
+// took the others' bits even where its own codes are 0.)  Queries are scaled by
+// a power of two; fp32 queries and their probabilities are split into hi + lo
+// columns.
 // Probabilities times vs are scaled by a power of two per step so that they
-// use fp16's range; each step's product starts afresh and joins the fp32
-// output with one fused multiply-add, so the tensor core's own sums stay short.
+// use fp16's range: 11 bits for fp16 and bf16 queries (an fp16 result has no
+// more, and the roundings of many rows average out; hi + lo would double the
+// columns), 22 for fp32 ones.  Each step's product starts afresh and joins the
+// fp32 output with one fused multiply-add, so the tensor core's own sums stay
+// short.
 //
 // Split.  The unit is 32 rows of one (request, kv head).  All units of the
 // call are dealt to the CTAs, one per SM, and in a CTA to its warps, as equal
@@ -139,7 +137,6 @@ template <int DT, int D, int NT>
 __global__ void __launch_bounds__(warps_of(D, NT, parts_of(DT)) * 32, 1) attend4_kernel(const AttendArgs a) {
   using T = typename Act<DT>::T;
   constexpr int PARTS = parts_of(DT);
-  constexpr bool EXACT = PARTS == 2;   // codes as exact integers, not offset subnormals
   constexpr int RB = 8 * NT / PARTS;   // rows of a block
   constexpr int NC = 2 / PARTS;        // rows a thread has per column tile
   constexpr int KW = D / 32;           // K words per thread and token
@@ -327,8 +324,7 @@ __global__ void __launch_bounds__(warps_of(D, NT, parts_of(DT)) * 32, 1) attend4
   float O[VW][4][2][NT][NC];   // [word][tile][row half][column tile][column]
   float mx[NT][NC], sum[NT][NC];
   int lim[NT][NC];             // last visible token
-  float cm = 0.f;              // scale log2(e) / the queries' power of two (and 2^24)
-  float s0[NT][2];             // a score's start value per column
+  float cm = 0.f;              // scale log2(e) / the queries' power of two
   float vscale = 1.f;          // O's power of two
 
   auto row_of = [&](int nt, int e) { return PARTS == 2 ? 4 * nt + t : 8 * nt + 2 * t + e; };
@@ -362,44 +358,29 @@ __global__ void __launch_bounds__(warps_of(D, NT, parts_of(DT)) * 32, 1) attend4
         }
       }
     }
-    float f = 1.f;
-    if (DT != PROX_F16) {
 #pragma unroll
-      for (int o = 16; o > 0; o >>= 1) top = max_nan(top, __shfl_xor_sync(0xffffffffu, top, o));
-      f = normaliser(top);
-    }
+    for (int o = 16; o > 0; o >>= 1) top = max_nan(top, __shfl_xor_sync(0xffffffffu, top, o));
+    const float f = normaliser(top);
     cm = c.scale * 1.4426950408889634f * inv_pow2(f);
-    if (!EXACT) cm *= 0x1p24f;
     vscale = 1.f;
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
-      float total = 0.f;  // of the column's Q as the products see it
 #pragma unroll
       for (int i = 0; i < KW; ++i) {
         uint32_t w[8];
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
-          // odd nibbles stand 4 bits higher in the subnormals
-          const float y = qv[nt][8 * i + j] * (!EXACT && (j & 1) ? 0.0625f * f : f);
+          const float y = qv[nt][8 * i + j] * f;
           const __half hi = __float2half_rn(y);
           __half v = hi;
           if (PARTS == 2 && (g & 1)) v = __float2half_rn(y - __half2float(hi));
           w[j] = __half_as_ushort(v);
-          total = fmaf(__half2float(v), j & 1 ? 16.f : 1.f, total);
         }
 #pragma unroll
         for (int h = 0; h < 2; ++h) {  // pairs (2h, 2h + 4) and (2h + 1, 2h + 5)
           qf[i][h][nt][0] = w[2 * h] | w[2 * h + 4] << 16;
           qf[i][h][nt][1] = w[2 * h + 1] | w[2 * h + 5] << 16;
         }
-      }
-      if (EXACT) {
-        s0[nt][0] = s0[nt][1] = 0.f;
-      } else {
-        total += __shfl_xor_sync(0xffffffffu, total, 1);
-        total += __shfl_xor_sync(0xffffffffu, total, 2);
-        s0[nt][0] = -0x1p-21f * __shfl_sync(0xffffffffu, total, 8 * t);
-        s0[nt][1] = -0x1p-21f * __shfl_sync(0xffffffffu, total, 8 * t + 4);
       }
 #pragma unroll
       for (int e = 0; e < NC; ++e) {
@@ -421,12 +402,6 @@ __global__ void __launch_bounds__(warps_of(D, NT, parts_of(DT)) * 32, 1) attend4
             for (int e = 0; e < NC; ++e) O[x][q][h][nt][e] = 0.f;
   };
 
-  auto decode = [&](uint32_t w, uint32_t(&r)[4]) {
-    if (EXACT)
-      widen8(w, r);
-    else
-      spread8(w, r);
-  };
   auto step = [&](const Cursor& s, int n, uint32_t st) {
     const int tok0 = s.c * kUnit, end = min(s.len, tok0 + n * kUnit);
     // the step's scales; rows behind the end may hold anything and count as 0
@@ -472,13 +447,12 @@ __global__ void __launch_bounds__(warps_of(D, NT, parts_of(DT)) * 32, 1) attend4
 #pragma unroll
       for (int i = 0; i < KW; ++i) {
         uint32_t ra[4], rb[4];
-        decode(w[0][i], ra);
-        decode(w[1][i], rb);
+        widen8(w[0][i], ra);
+        widen8(w[1][i], rb);
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
           if (i == 0)
-            mma_f16(S[m][nt], ra[0], rb[0], ra[1], rb[1], qf[i][0][nt][0], qf[i][0][nt][1], s0[nt][0], s0[nt][1],
-                    s0[nt][0], s0[nt][1]);
+            mma_f16(S[m][nt], ra[0], rb[0], ra[1], rb[1], qf[i][0][nt][0], qf[i][0][nt][1], 0.f, 0.f, 0.f, 0.f);
           else
             mma_f16(S[m][nt], ra[0], rb[0], ra[1], rb[1], qf[i][0][nt][0], qf[i][0][nt][1]);
           mma_f16(S[m][nt], ra[2], rb[2], ra[3], rb[3], qf[i][1][nt][0], qf[i][1][nt][1]);
@@ -567,20 +541,7 @@ __global__ void __launch_bounds__(warps_of(D, NT, parts_of(DT)) * 32, 1) attend4
     }
     vscale = vf;
 
-    // O^T += V^T P^T: thread g has VW words of 8 values of each token.  Start
-    // values: -8 sum_j p_j 2^-24, 16 times that in the rows of odd nibbles.
-    float o0[NT][4];
-#pragma unroll
-    for (int nt = 0; nt < NT; ++nt) {
-      if (EXACT) {
-        o0[nt][0] = o0[nt][1] = o0[nt][2] = o0[nt][3] = 0.f;
-      } else {
-        mma_f16(o0[nt], 0x80088008u, 0x80808080u, 0x80088008u, 0x80808080u, pf[0][nt][0], pf[0][nt][1], 0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-        for (int m = 1; m < MT; ++m)
-          mma_f16(o0[nt], 0x80088008u, 0x80808080u, 0x80088008u, 0x80808080u, pf[m][nt][0], pf[m][nt][1]);
-      }
-    }
+    // O^T += V^T P^T: thread g has VW words of 8 values of each token
     const uint32_t sv = st + ROWS * (D / 2);
 #pragma unroll
     for (int x0 = 0; x0 < VW; x0 += 2) {  // two words at a time (head_dim 64 has one)
@@ -607,16 +568,16 @@ __global__ void __launch_bounds__(warps_of(D, NT, parts_of(DT)) * 32, 1) attend4
 #pragma unroll
           for (int half = 0; half < 2; ++half) {  // values 8x + 4 half .. + 3 of the thread
             uint32_t r0[4], r1[4];
-            decode(prmt(vw[0][x], vw[1][x], half ? 0x7632 : 0x5410), r0);
-            decode(prmt(vw[2][x], vw[3][x], half ? 0x7632 : 0x5410), r1);
+            widen8(prmt(vw[0][x], vw[1][x], half ? 0x7632 : 0x5410), r0);
+            widen8(prmt(vw[2][x], vw[3][x], half ? 0x7632 : 0x5410), r1);
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) {
               float(&d0)[4] = part[x][2 * half][nt];
               float(&d1)[4] = part[x][2 * half + 1][nt];
               const uint32_t b0 = pf[m][nt][0], b1 = pf[m][nt][1];
               if (m == 0) {
-                mma_f16(d0, r0[0], r0[1], r1[0], r1[1], b0, b1, o0[nt][0], o0[nt][1], o0[nt][2], o0[nt][3]);
-                mma_f16(d1, r0[2], r0[3], r1[2], r1[3], b0, b1, o0[nt][0], o0[nt][1], o0[nt][2], o0[nt][3]);
+                mma_f16(d0, r0[0], r0[1], r1[0], r1[1], b0, b1, 0.f, 0.f, 0.f, 0.f);
+                mma_f16(d1, r0[2], r0[3], r1[2], r1[3], b0, b1, 0.f, 0.f, 0.f, 0.f);
               } else {
                 mma_f16(d0, r0[0], r0[1], r1[0], r1[1], b0, b1);
                 mma_f16(d1, r0[2], r0[3], r1[2], r1[3], b0, b1);
@@ -648,10 +609,10 @@ __global__ void __launch_bounds__(warps_of(D, NT, parts_of(DT)) * 32, 1) attend4
 #pragma unroll
       for (int q = 0; q < 4; ++q)
 #pragma unroll
-        for (int h = 0; h < 2; ++h) y[8 * x + 2 * q + h] = O[x][q][h][nt][e] * (!EXACT && h ? 0.0625f * f : f);
+        for (int h = 0; h < 2; ++h) y[8 * x + 2 * q + h] = O[x][q][h][nt][e] * f;
   };
   auto end_rows = [&](const Cursor& s, float* slot) {
-    const float unscale = (EXACT ? 1.f : 0x1p24f) * inv_pow2(vscale);
+    const float unscale = inv_pow2(vscale);
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll

@@ -113,14 +113,8 @@ __device__ __forceinline__ int range_of(int U, int u, int W) {
 // in bits 0-1 of the other half, so that a rotation by 8 brings D to 6-9 and C
 // to 2-5.  r: A fragments in the order a0 (B), a1 (C), a2 (A), a3 (D), as
 // integers q: in the mantissas of 256 and of 16 the fields are 256 + n and
-// 16 + n.
-// (w & mask) | bits, as one instruction (left to the compiler it became two:
-// 34.6 us for 28672 x 8192 at 5 tokens instead of 28.8).
-__device__ __forceinline__ uint32_t and_or(uint32_t w, uint32_t mask, uint32_t bits) {
-  uint32_t r;
-  asm("lop3.b32 %0, %1, %2, %3, 0xEA;" : "=r"(r) : "r"(w), "r"(mask), "r"(bits));
-  return r;
-}
+// 16 + n.  (Without the fused and_or 28672 x 8192 took 34.6 us at 5 tokens
+// instead of 28.8.)
 __device__ __forceinline__ void decode_words(uint32_t w, uint32_t (&r)[4]) {
   const uint32_t rot = __funnelshift_r(w, w, 8);
   const __half2 low = bits_h2(0xDC20DC20u), high = bits_h2(0xCE00CE00u);  // -264, -24

@@ -3,9 +3,9 @@
 // product on them.
 //
 // Codes are held as q + 8 in a nibble.  A nibble ORed into the mantissa of
-// 1024.0 (0x6400) is the fp16 number 1024 + n, so one fp16 subtraction gives
-// the exact integer q for two codes at once; a nibble 4 bits higher is
-// 1024 + 16 n, and one fused multiply-add brings it to q as well.  |q| <= 8 is
+// 1024.0 (0x6400) is the fp16 number 1024 + n, and 4 bits higher in that of 64.0
+// (0x5400) it is 64 + n, so one fp16 subtraction gives the exact integer q for
+// two codes at once.  |q| <= 8 is
 // exact in fp16, products with fp16 operands are exact in the tensor core's
 // fp32 sum, and the scales are applied to sums in fp32.
 #pragma once
@@ -23,15 +23,22 @@ namespace q4 {
 __device__ __forceinline__ uint32_t h2_bits(__half2 h) { return *reinterpret_cast<uint32_t*>(&h); }
 __device__ __forceinline__ __half2 bits_h2(uint32_t w) { return *reinterpret_cast<__half2*>(&w); }
 
+// (w & mask) | bits, as one instruction (left to the compiler it may become two).
+__device__ __forceinline__ uint32_t and_or(uint32_t w, uint32_t mask, uint32_t bits) {
+  uint32_t r;
+  asm("lop3.b32 %0, %1, %2, %3, 0xEA;" : "=r"(r) : "r"(w), "r"(mask), "r"(bits));
+  return r;
+}
+
 // The codes at nibbles 0 and 4 (SHIFTED = false) or 1 and 5 (true) of w, as
 // two fp16 integers in [-8, 7].
 template <bool SHIFTED>
 __device__ __forceinline__ uint32_t widen(uint32_t w) {
   if (SHIFTED) {
-    const uint32_t m = (w & 0x00F000F0u) | 0x64006400u;  // 1024 + 16 n
-    return h2_bits(__hfma2(bits_h2(m), bits_h2(0x2C002C00u), bits_h2(0xD480D480u)));  // m / 16 - 72
+    const uint32_t m = and_or(w, 0x00F000F0u, 0x54005400u);  // 64 + n
+    return h2_bits(__hsub2(bits_h2(m), bits_h2(0x54805480u)));  // m - 72
   }
-  const uint32_t m = (w & 0x000F000Fu) | 0x64006400u;  // 1024 + n
+  const uint32_t m = and_or(w, 0x000F000Fu, 0x64006400u);  // 1024 + n
   return h2_bits(__hsub2(bits_h2(m), bits_h2(0x64086408u)));  // m - 1032
 }
 
@@ -43,21 +50,6 @@ __device__ __forceinline__ void widen8(uint32_t w, uint32_t (&r)[4]) {
   w >>= 8;
   r[2] = widen<false>(w);
   r[3] = widen<true>(w);
-}
-
-// The word's nibbles as fp16 subnormals: n 2^-24 in r[0] = nibbles (0, 4) and
-// r[2] = (2, 6), 16 n 2^-24 in r[1] = (1, 5) and r[3] = (3, 7).  A nibble in the
-// low mantissa bits of an fp16 zero IS that number, so this is five logical
-// instructions for eight codes; the factor 16 goes into the other operand and
-// the offset 8 into the sum's start value.  The tensor core aligns products by
-// their factors' exponents, a subnormal's being 2^-14: sums of n 2^-24 x are
-// held to 2^-14 of a code step of the largest x (seen: 2^-14.3).
-__device__ __forceinline__ void spread8(uint32_t w, uint32_t (&r)[4]) {
-  r[0] = w & 0x000F000Fu;
-  r[1] = w & 0x00F000F0u;
-  w >>= 8;
-  r[2] = w & 0x000F000Fu;
-  r[3] = w & 0x00F000F0u;
 }
 
 // D[16 x 8] += A[16 x 16] B[16 x 8], fp16 operands, fp32 sums.

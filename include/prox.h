@@ -467,10 +467,11 @@ PROX_API prox_status prox_kv4_read(const prox_kv4* cache, const int64_t* slots, 
  * < 2^36; scale finite.  An entry outside [0, num_pages) sets
  * PROX_DEVERR_PAGE, a length outside [0, cols * page_size] PROX_DEVERR_LEN;
  * that request's result is then meaningless, and no memory outside the cache
- * is touched.  Softmax statistics, outputs and the sums over rows are fp32; fp16
- * and bf16 queries enter the products as they are, probabilities with 11 bits,
- * and sums of up to 64 rows are good to 2^-14 of a code step; for fp32 queries
- * both carry 22.  Results do not depend on timing. */
+ * is touched.  Codes enter the products as integers; softmax statistics, scores,
+ * outputs and the sums over rows are fp32.  fp16 and bf16 queries enter in full
+ * (down to 2^-25 of the largest magnitude beside them), fp32 queries with 22 bits;
+ * probabilities carry 11 bits, for fp32 queries 22.  Results do not depend on
+ * timing. */
 PROX_API prox_status prox_kv4_attend(const prox_kv4* cache, const void* q, int64_t q_req, int64_t q_tok,
                                      int64_t q_head, int n_q_heads, int B, int Tq, const int32_t* table,
                                      int64_t table_stride, int cols, const int32_t* lens, float scale, void* out,

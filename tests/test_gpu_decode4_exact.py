@@ -8,7 +8,7 @@ import torch
 
 import activation_sparse_swiglu_b200 as prox
 from tests import decode4_helpers as ref
-from tests.test_gpu_decode4 import linear_case, within
+from tests.test_gpu_decode4 import attend_case, gen_of, linear_case, within
 
 pytestmark = pytest.mark.gpu
 HALVES = [torch.float16, torch.bfloat16]
@@ -53,3 +53,90 @@ def test_linear4_sums_are_fp32(K, N, B, dtype):
     codes, scales, x = linear_case(prox, K, N, B, dtype, seed=K + N + B, spread=30.0)
     want, tol = linear4(x, codes, scales)
     within(prox.Linear4(codes=codes, scales=scales)(x), want, tol)
+
+
+def attend(q, cache, table, lens, scale):
+    """Attention in 64 bits and the bound on a result's error for 16-bit q.
+    Scores: sums of D products in fp32 (D / 16 tensor core steps), 4 more
+    roundings; q is exact down to 2^-25 of its row's largest magnitude and has a
+    step of 2^-38 of it below.  Weights: rounded to 11 bits, an exponential good
+    to 2^-22.  Outputs: steps of at most 64 rows of 4 tensor core steps each,
+    joined at most 12 + 148 times; a weight below 2^-28 of its step's largest has
+    a step of 2^-38 of it.  The result is rounded once."""
+    B, Tq, Hq, D = q.shape
+    Hkv, page = cache.k_scales.shape[1], cache.k_scales.shape[2]
+    G = Hq // Hkv
+    out = torch.zeros((B, Tq, Hq, D), dtype=torch.float64, device=q.device)
+    tol = torch.zeros_like(out)
+    for b, n in enumerate(lens.tolist()):
+        ids = table[b, :-(-n // page)].long()
+        for h in range(Hkv):
+            k, v = ((ref.unpack(c[ids, h]).double() * s[ids, h].double()[..., None]).flatten(0, 1)[:n]
+                    for c, s in ((cache.k_codes, cache.k_scales), (cache.v_codes, cache.v_scales)))
+            for i in range(Tq):
+                m = n - Tq + i + 1
+                if m <= 0:
+                    continue
+                at = (b, i, slice(h * G, (h + 1) * G))
+                qd = q[at].double()
+                p = torch.softmax(qd @ k[:m].T * scale, -1)
+                out[at] = p @ v[:m]
+                e = (D / 16 + 6) * 2.0 ** -23 * (qd.abs() @ k[:m].abs().T).amax(-1, keepdim=True)
+                e = abs(scale) * (e + 2.0 ** -38 * qd.abs().amax(-1, keepdim=True) * k[:m].abs().sum(-1).max())
+                rel = 2 * e + 2.0 ** -11 + 2.0 ** -22 + (m / 16 + 180) * 2.0 ** -23
+                tol[at] = rel * (p @ v[:m].abs()) + m * 2.0 ** -38 * v[:m].abs().max() + ref.HALF_STEP[q.dtype] * out[at].abs()
+    return out, tol + (2.0 ** -24 if q.dtype == torch.float16 else 0.0)
+
+
+def check(case, scale=None):
+    cache, q, table, lens = case
+    scale = q.shape[-1] ** -0.5 if scale is None else scale
+    want, tol = attend(q, cache, table, lens, scale)
+    within(cache.attend(q, table, lens, scale=scale), want, tol)
+
+
+@pytest.mark.parametrize("dtype", HALVES)
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("lens, Tq, Hkv, G, page", [([1, 37], 1, 4, 2, 16), ([200, 3000, 64], 1, 2, 4, 32),
+                                                    ([17, 250, 0, 2], 3, 2, 4, 16), ([700, 90], 5, 2, 7, 64)])
+def test_attend_sums_are_fp32(lens, Tq, Hkv, G, page, D, dtype):
+    check(attend_case(prox, lens, Tq, Hkv, G, D, page, dtype, seed=sum(lens) + D))
+
+
+@pytest.mark.parametrize("dtype", HALVES)
+@pytest.mark.parametrize("D", [64, 128, 256])
+def test_attend_large_query_elements_at_zero_codes(D, dtype):
+    """Query elements far above the others where every key's code is 0: the
+    scores are made of the others."""
+    cache, q, table, lens = attend_case(prox, [300, 64, 5], 2, 2, 3, D, 32, dtype, seed=D)
+    for d, large in ((2, 1e4), (D - 1, -3e4)):  # an even and an odd element
+        codes = cache.k_codes[..., d // 2]
+        cache.k_codes[..., d // 2] = codes & 0xF0 | 0x08 if d % 2 == 0 else codes & 0x0F | 0x80
+        q[..., d] = large
+    check((cache, q, table, lens))
+
+
+@pytest.mark.parametrize("dtype", HALVES)
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("score", [8.0, 16.0])
+def test_attend_heavy_row_of_zero_codes(score, D, dtype):
+    """A row with nearly all of the weight whose value codes are 0 in one half:
+    there the result is made of the other rows."""
+    cache, q, table, lens = attend_case(prox, [400, 70], 1, 1, 4, D, 16, dtype, seed=D + 1)
+    q.copy_(torch.randn(q.shape, device="cuda", generator=gen_of(1)).sign())  # q . q = D
+    for b, j in ((0, 123), (1, 0)):
+        page, row = int(table[b, j // 16]), j % 16
+        cache.k_codes[page, 0, row] = ref.pack(7 * q[b, 0, 0].long())[None]
+        cache.k_scales[page, 0, row] = score / (7.0 * D ** 0.5)  # head 0's score for it
+        cache.v_codes[page, 0, row, :D // 4] = 0x88
+    check((cache, q, table, lens))
+
+
+@pytest.mark.parametrize("dtype", HALVES)
+@pytest.mark.parametrize("small", [1e-3, 1e-4, 1e-5])
+def test_attend_small_queries_under_a_large_scale(small, dtype):
+    """Queries near the end of fp16's range keep their bits; the scale brings
+    their scores to the usual size."""
+    for D in (64, 128, 256):
+        cache, q, table, lens = attend_case(prox, [300, 33], 1, 2, 4, D, 32, torch.float32, seed=D + 2)
+        check((cache, (q * small).to(dtype), table, lens), scale=D ** -0.5 / small)
