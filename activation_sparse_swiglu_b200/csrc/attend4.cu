@@ -22,8 +22,9 @@
 // code), so products are exact and sums are fp32.  (A nibble masked out of a
 // word is an fp16 subnormal, 5/8 of an instruction; but the tensor core aligns
 // products by their factors' exponents, so a large query element or a heavy row
-// took the others' bits even where its own codes are 0.)  Queries are scaled by
-// a power of two; fp32 queries and their probabilities are split into hi + lo
+// took the others' bits even where its own codes are 0.)  Each bf16 or fp32
+// query row is scaled by a power of two of its own, so that no head takes bits
+// from another; fp32 queries and their probabilities are split into hi + lo
 // columns.
 // Probabilities times vs are scaled by a power of two per step so that they
 // use fp16's range: 11 bits for fp16 and bf16 queries (an fp16 result has no
@@ -323,8 +324,8 @@ __global__ void __launch_bounds__(warps_of(D, NT, parts_of(DT)) * 32, 1) attend4
   uint32_t qf[KW][2][NT][2];
   float O[VW][4][2][NT][NC];   // [word][tile][row half][column tile][column]
   float mx[NT][NC], sum[NT][NC];
-  int lim[NT][NC];             // last visible token
-  float cm = 0.f;              // scale log2(e) / the queries' power of two
+  float cm = 0.f;              // scale log2(e) / the smallest of the rows' powers of two
+  float rf[NT][NC];            // that one / the row's own (fp16 queries enter as they are: 1)
   float vscale = 1.f;          // O's power of two
 
   auto row_of = [&](int nt, int e) { return PARTS == 2 ? 4 * nt + t : 8 * nt + 2 * t + e; };
@@ -340,9 +341,11 @@ __global__ void __launch_bounds__(warps_of(D, NT, parts_of(DT)) * 32, 1) attend4
 
   auto begin_rows = [&](const Cursor& s) {
     float qv[NT][KW * 8];
-    float top = 0.f;
+    float f[NT];                // of the lane's rows
+    float least = 0x1p126f;     // of all rows that are neither zero nor non-finite
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
+      float top = 0.f;
       const int r = s.block * RB + (PARTS == 2 ? 4 * nt + (g >> 1) : 8 * nt + g), i0 = token_of_row(r);
       const T* q = static_cast<const T*>(c.q) + s.b * c.q_req + i0 * c.q_tok +
                    (s.head * a.G + (r - i0 * a.G)) * c.q_head;
@@ -357,11 +360,23 @@ __global__ void __launch_bounds__(warps_of(D, NT, parts_of(DT)) * 32, 1) attend4
           top = max_nan(top, fabsf(x[j]));
         }
       }
+#pragma unroll
+      for (int o = 1; o < 4; o <<= 1) top = max_nan(top, __shfl_xor_sync(0xffffffffu, top, o));
+      f[nt] = DT == PROX_F16 ? 1.f : normaliser(top);
+      if (top > 0.f && top < INFINITY) least = fminf(least, f[nt]);
     }
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) top = max_nan(top, __shfl_xor_sync(0xffffffffu, top, o));
-    const float f = normaliser(top);
-    cm = c.scale * 1.4426950408889634f * inv_pow2(f);
+    for (int o = 4; o < 32; o <<= 1) least = fminf(least, __shfl_xor_sync(0xffffffffu, least, o));
+    // The scores of the row with the smallest power (the largest queries) are
+    // cm ks z; the other rows' come out larger by their rf's inverse, which the
+    // softmax takes off.  (At least 2^-126: a masked score, -inf, stays that.)
+    cm = c.scale * 1.4426950408889634f * inv_pow2(DT == PROX_F16 ? 1.f : least);
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+      const float own = fmaxf(inv_pow2(f[nt]) * least, 0x1p-126f);
+#pragma unroll
+      for (int e = 0; e < NC; ++e) rf[nt][e] = DT == PROX_F16 ? 1.f : __shfl_sync(0xffffffffu, own, 8 * t + 4 * e);
+    }
     vscale = 1.f;
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
@@ -370,7 +385,7 @@ __global__ void __launch_bounds__(warps_of(D, NT, parts_of(DT)) * 32, 1) attend4
         uint32_t w[8];
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
-          const float y = qv[nt][8 * i + j] * f;
+          const float y = qv[nt][8 * i + j] * f[nt];
           const __half hi = __float2half_rn(y);
           __half v = hi;
           if (PARTS == 2 && (g & 1)) v = __float2half_rn(y - __half2float(hi));
@@ -384,8 +399,6 @@ __global__ void __launch_bounds__(warps_of(D, NT, parts_of(DT)) * 32, 1) attend4
       }
 #pragma unroll
       for (int e = 0; e < NC; ++e) {
-        const int r = s.block * RB + row_of(nt, e);
-        lim[nt][e] = r < a.R ? s.len - c.Tq + token_of_row(r) : s.len - 1;
         mx[nt][e] = -INFINITY;
         sum[nt][e] = 0.f;
       }
@@ -402,6 +415,11 @@ __global__ void __launch_bounds__(warps_of(D, NT, parts_of(DT)) * 32, 1) attend4
             for (int e = 0; e < NC; ++e) O[x][q][h][nt][e] = 0.f;
   };
 
+  // Last token that a row sees (worked out where a step needs it: registers are scarcer).
+  auto last_of = [&](const Cursor& s, int nt, int e) {
+    const int r = s.block * RB + row_of(nt, e);
+    return r < a.R ? s.len - c.Tq + token_of_row(r) : s.len - 1;
+  };
   auto step = [&](const Cursor& s, int n, uint32_t st) {
     const int tok0 = s.c * kUnit, end = min(s.len, tok0 + n * kUnit);
     // the step's scales; rows behind the end may hold anything and count as 0
@@ -487,20 +505,23 @@ __global__ void __launch_bounds__(warps_of(D, NT, parts_of(DT)) * 32, 1) attend4
           }
       if (masked) {
 #pragma unroll
-        for (int m = 0; m < MT; ++m)
+        for (int e = 0; e < NC; ++e) {
+          const int last = min(last_of(s, nt, e), end - 1) - tok0 - tr;
 #pragma unroll
-          for (int h = 0; h < 2; ++h)
+          for (int m = 0; m < MT; ++m)
 #pragma unroll
-            for (int e = 0; e < NC; ++e)
-              if (tok0 + 16 * m + 8 * h + tr > min(lim[nt][e], end - 1)) p[m][h][e] = -INFINITY;
+            for (int h = 0; h < 2; ++h)
+              if (16 * m + 8 * h > last) p[m][h][e] = -INFINITY;
+        }
       }
 #pragma unroll
       for (int e = 0; e < NC; ++e) {
-        float top = mx[nt][e];
+        float top = -INFINITY;
 #pragma unroll
         for (int m = 0; m < MT; ++m) top = fmaxf(top, fmaxf(p[m][0][e], p[m][1][e]));
 #pragma unroll
         for (int o = 4; o < 32; o <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+        top = fmaxf(mx[nt][e], top * rf[nt][e]);
         const float base = top == -INFINITY ? 0.f : top;
         const float al = exp2_fast(mx[nt][e] - base);
         mx[nt][e] = top;
@@ -509,7 +530,7 @@ __global__ void __launch_bounds__(warps_of(D, NT, parts_of(DT)) * 32, 1) attend4
         for (int m = 0; m < MT; ++m)
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
-            const float y = exp2_fast(p[m][h][e] - base);
+            const float y = exp2_fast(fmaf(p[m][h][e], rf[nt][e], -base));
             add += y;
             p[m][h][e] = y * vsc[m][h];
           }
@@ -518,12 +539,14 @@ __global__ void __launch_bounds__(warps_of(D, NT, parts_of(DT)) * 32, 1) attend4
       }
       if (masked) {  // an infinite or NaN scale of a masked row times 0 is NaN
 #pragma unroll
-        for (int m = 0; m < MT; ++m)
+        for (int e = 0; e < NC; ++e) {
+          const int last = min(last_of(s, nt, e), end - 1) - tok0 - tr;
 #pragma unroll
-          for (int h = 0; h < 2; ++h)
+          for (int m = 0; m < MT; ++m)
 #pragma unroll
-            for (int e = 0; e < NC; ++e)
-              if (tok0 + 16 * m + 8 * h + tr > min(lim[nt][e], end - 1)) p[m][h][e] = 0.f;
+            for (int h = 0; h < 2; ++h)
+              if (16 * m + 8 * h > last) p[m][h][e] = 0.f;
+        }
       }
 #pragma unroll
       for (int m = 0; m < MT; ++m)

@@ -469,9 +469,9 @@ PROX_API prox_status prox_kv4_read(const prox_kv4* cache, const int64_t* slots, 
  * that request's result is then meaningless, and no memory outside the cache
  * is touched.  Codes enter the products as integers; softmax statistics, scores,
  * outputs and the sums over rows are fp32.  fp16 and bf16 queries enter in full
- * (down to 2^-25 of the largest magnitude beside them), fp32 queries with 22 bits;
- * probabilities carry 11 bits, for fp32 queries 22.  Results do not depend on
- * timing. */
+ * (down to 2^-25 of their row's largest magnitude), fp32 queries with 22 bits;
+ * probabilities carry 11 bits, for fp32 queries 22.  A query with a NaN gives NaN;
+ * other queries are not touched by it.  Results do not depend on timing. */
 PROX_API prox_status prox_kv4_attend(const prox_kv4* cache, const void* q, int64_t q_req, int64_t q_tok,
                                      int64_t q_head, int n_q_heads, int B, int Tq, const int32_t* table,
                                      int64_t table_stride, int cols, const int32_t* lens, float scale, void* out,

@@ -1,7 +1,10 @@
-"""What 16-bit inputs of the 4-bit operators must not lose: codes enter the
-products as integers, so a large input costs its small neighbours nothing where
-its own codes are 0.  Against plain forms in 64 bits, with bounds that count
-fp32 sums and each rounding."""
+"""What inputs of the 4-bit operators must not lose.  Codes enter the products as
+integers, so a large 16-bit input costs its small neighbours nothing where its
+own codes are 0; query rows have powers of two of their own, so no head costs
+another.  Against plain forms in 64 bits, with bounds that count fp32 sums and
+each rounding."""
+
+import math
 
 import pytest
 import torch
@@ -140,3 +143,56 @@ def test_attend_small_queries_under_a_large_scale(small, dtype):
     for D in (64, 128, 256):
         cache, q, table, lens = attend_case(prox, [300, 33], 1, 2, 4, D, 32, torch.float32, seed=D + 2)
         check((cache, (q * small).to(dtype), table, lens), scale=D ** -0.5 / small)
+
+
+@pytest.mark.parametrize("dtype", ref.TYPES)
+@pytest.mark.parametrize("G, Tq, D", [(4, 1, 64), (4, 1, 128), (3, 3, 128), (5, 1, 256)])
+@pytest.mark.parametrize("bad", [float("nan"), float("inf"), -float("inf")])
+def test_attend_non_finite_query_leaves_its_block_as_it_was(bad, G, Tq, D, dtype):
+    """Every other query of the block has the same bits as without it, queries
+    past fp16's range among them."""
+    cache, q, table, lens = attend_case(prox, [400, 40], Tq, 1, G, D, 16, dtype, seed=G + D)
+    size = 1.0 if dtype == torch.float16 else 2.0 ** 20
+    q = q * size
+    want = cache.attend(q, table, lens, scale=D ** -0.5 / size)
+    assert torch.isfinite(want).all()
+    for i, h in ((0, 0), (Tq - 1, G - 1)):
+        q2 = q.clone()
+        q2[0, i, h, 3] = bad
+        got = cache.attend(q2, table, lens, scale=D ** -0.5 / size)
+        assert not torch.isfinite(got[0, i, h]).any()
+        got[0, i, h] = want[0, i, h]
+        assert torch.equal(got, want)
+
+
+@pytest.mark.parametrize("dtype", ref.TYPES)
+@pytest.mark.parametrize("D", [64, 128, 256])
+def test_attend_heads_of_very_different_size(D, dtype):
+    """Heads of one group whose queries differ by many orders: each is as good
+    as alone, at the scale that brings its scores to the usual size."""
+    steps = [0, 8, 16] if dtype == torch.float16 else [0, 20, 40, 60]
+    cache, q, table, lens = attend_case(prox, [300, 33], 1, 2, len(steps), D, 32, torch.float32, seed=D + 3)
+    for j, e in enumerate(steps):
+        q[:, :, j::len(steps)] *= 2.0 ** -e
+    q = q.to(dtype)
+    for e in steps:
+        scale = D ** -0.5 * 2.0 ** e
+        if dtype == torch.float32:
+            want, _, tol, _ = ref.attend(q, cache.k_codes, cache.k_scales, cache.v_codes, cache.v_scales, table, lens,
+                                         scale)
+        else:
+            want, tol = attend(q, cache, table, lens, scale)
+        within(cache.attend(q, table, lens, scale=scale), want, tol)
+
+
+@pytest.mark.parametrize("dtype", ref.TYPES)
+def test_attend_zero_queries_beside_others(dtype):
+    """A query of zeros weighs all its rows alike, whatever the others are."""
+    cache, q, table, lens = attend_case(prox, [300], 1, 1, 4, 128, 32, dtype, seed=5)
+    q[:, :, 1] = 0
+    q[:, :, 2] *= 1e-4
+    for q in (q, torch.zeros_like(q)):
+        want, tol = attend(q, cache, table, lens, 128 ** -0.5)  # (for fp32 wider than it need be)
+        lse = torch.empty((1, 1, 4), device="cuda")
+        within(cache.attend(q, table, lens, lse=lse), want, tol)
+        assert abs(float(lse[0, 0, 1]) - math.log(300)) <= 2.0 ** -20
