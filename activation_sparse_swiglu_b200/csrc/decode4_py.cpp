@@ -11,6 +11,7 @@
 #include <cstdint>
 
 #include <ATen/Functions.h>
+#include <ATen/core/grad_mode.h>
 #include <ATen/core/LegacyTypeDispatch.h>
 #include <c10/cuda/CUDAFunctions.h>
 #include <c10/cuda/CUDAStream.h>
@@ -74,12 +75,20 @@ void on(const at::Tensor& t, int index, const char* name) {
 int code_of(at::ScalarType t) {
   return t == at::kFloat ? PROX_F32 : t == at::kHalf ? PROX_F16 : t == at::kBFloat16 ? PROX_BF16 : -1;
 }
+// The calls give no gradients: a tensor whose gradient or tangent they would
+// drop is refused.
+void no_gradient(const at::Tensor& t, const char* name) {
+  if ((t.requires_grad() && at::GradMode::is_enabled()) || t._fw_grad(0).defined())
+    RAISE(PyExc_RuntimeError,
+          "%s carries a gradient, which this operator does not give: detach it or call under torch.no_grad()", name);
+}
 // An activation tensor on the device, and its type's code.
 const at::Tensor& act(PyObject* o, int index, const char* name, int* code) {
   const at::Tensor& t = tensor(o, name);
   *code = code_of(t.scalar_type());
   if (*code < 0) RAISE(PyExc_TypeError, "%s must be float32, float16 or bfloat16", name);
   on(t, index, name);
+  no_gradient(t, name);
   return t;
 }
 // A contiguous tensor of `numel` integers on the device.
@@ -147,6 +156,7 @@ PyObject* linear4_forward(PyObject*, PyObject* const* a, Py_ssize_t n) {
     } else {
       out = &tensor(a[5], "out");
       on(*out, index, "out");
+      no_gradient(*out, "out");
       if (out->scalar_type() != x.scalar_type() || out->dim() != dim || out->size(-1) != d_out || out->stride(-1) != 1 ||
           (dim == 2 && out->size(0) != B))
         RAISE(PyExc_ValueError, "out must be of x's type, %lld rows of %lld contiguous values", (long long)B,
@@ -236,6 +246,7 @@ PyObject* kv4_attend(PyObject*, PyObject* const* a, Py_ssize_t n) {
     } else {
       out = &tensor(a[7], "out");
       on(*out, index, "out");
+      no_gradient(*out, "out");
       if (out->scalar_type() != q.scalar_type() || out->sizes() != q.sizes() || !out->is_contiguous())
         RAISE(PyExc_ValueError, "out must be a contiguous tensor of q's shape and type");
     }
@@ -243,6 +254,7 @@ PyObject* kv4_attend(PyObject*, PyObject* const* a, Py_ssize_t n) {
     if (a[8] != Py_None) {
       const at::Tensor& t = tensor(a[8], "lse");
       on(t, index, "lse");
+      no_gradient(t, "lse");
       if (t.scalar_type() != at::kFloat || t.numel() != B * Tq * Hq || !t.is_contiguous())
         RAISE(PyExc_ValueError, "lse must hold %lld contiguous float32 values", (long long)(B * Tq * Hq));
       lse = t.data_ptr<float>();

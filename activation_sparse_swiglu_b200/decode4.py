@@ -7,6 +7,9 @@ plan of the pages and slots that a step's tokens take.
     cache.append(k, v, plan.slots)
     o = cache.attend(q, table, plan.lens)              # [B, Hq, D]
 
+No call gives gradients: one whose inputs carry them (outside torch.no_grad())
+is refused.
+
 Argument checks and marshalling only, most of it in the native module _decode4
 (csrc/decode4_py.cpp); the arithmetic runs in libprox.so.
 """
