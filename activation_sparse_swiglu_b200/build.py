@@ -9,6 +9,7 @@ from __future__ import annotations
 
 import argparse
 import os
+import re
 import shutil
 import subprocess
 import sys
@@ -77,19 +78,37 @@ def build(force: bool = False, verbose: bool = False, ptxas_info: bool = False) 
     return LIB
 
 
+def _torch_dir() -> str:
+    import importlib.util
+    return os.path.dirname(importlib.util.find_spec("torch").origin)
+
+
+def entry_tag() -> str:
+    """What _decode4.so is compiled against: its C++ interface is that of one
+    torch and one Python."""
+    with open(os.path.join(_torch_dir(), "version.py")) as fh:
+        version = re.search(r"^__version__ = '([^']*)'", fh.read(), re.M).group(1)
+    return f"torch {version}, {sys.implementation.cache_tag}"
+
+
+def entry_up_to_date() -> bool:
+    inputs = [ENTRY_SOURCE, os.path.join(INCLUDE, "prox.h"), os.path.abspath(__file__)]
+    if not os.path.exists(ENTRY) or any(os.path.getmtime(f) > os.path.getmtime(ENTRY) for f in inputs):
+        return False
+    with open(ENTRY, "rb") as fh:
+        return entry_tag().encode() + b"\0" in fh.read()
+
+
 def build_entry(force: bool = False, verbose: bool = False) -> str:
     """_decode4.so: a CPython module over torch's tensors and libprox.so."""
-    inputs = [ENTRY_SOURCE, os.path.join(INCLUDE, "prox.h"), os.path.abspath(__file__)]
-    if not force and os.path.exists(ENTRY) and all(
-            os.path.getmtime(f) <= os.path.getmtime(ENTRY) for f in inputs):
+    if not force and entry_up_to_date():
         return ENTRY
-    import importlib.util
     import sysconfig
-    torch_dir = os.path.dirname(importlib.util.find_spec("torch").origin)
+    torch_dir = _torch_dir()
     cuda = os.path.dirname(os.path.dirname(os.path.realpath(_nvcc())))
     tmp = ENTRY + ".tmp"
     cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden", "-o", tmp, ENTRY_SOURCE,
-           "-I", INCLUDE, "-isystem", os.path.join(torch_dir, "include"),
+           f'-DPROX_BUILT_FOR="{entry_tag()}"', "-I", INCLUDE, "-isystem", os.path.join(torch_dir, "include"),
            "-isystem", os.path.join(torch_dir, "include", "torch", "csrc", "api", "include"),
            "-isystem", sysconfig.get_paths()["include"], "-isystem", os.path.join(cuda, "include"),
            "-L", PKG, "-l:libprox.so", "-L", os.path.join(torch_dir, "lib"), "-ltorch_python", "-ltorch_cpu",

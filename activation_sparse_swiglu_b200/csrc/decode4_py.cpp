@@ -338,6 +338,11 @@ PyModuleDef module = {PyModuleDef_HEAD_INIT, "_decode4", "Calls of the 4-bit ope
 PyMODINIT_FUNC PyInit__decode4(void) {
   PyObject* m = PyModule_Create(&module);
   if (!m) return nullptr;
+  // what this module's C++ interface is that of (see build.py); checked before any call
+  if (PyModule_AddStringConstant(m, "built_for", PROX_BUILT_FOR) < 0) {
+    Py_DECREF(m);
+    return nullptr;
+  }
   // _lib.py loads libprox.so and defines the error before this module is imported
   PyObject* lib = PyImport_ImportModule("activation_sparse_swiglu_b200._lib");
   prox_error = lib ? PyObject_GetAttrString(lib, "ProxError") : nullptr;

@@ -18,6 +18,7 @@ from __future__ import annotations
 
 import ctypes
 import math
+import sys
 from typing import NamedTuple
 
 import torch
@@ -26,9 +27,12 @@ from ._lib import PKG, check, lib
 
 try:
     from . import _decode4
+    _tag = f"torch {torch.__version__}, {sys.implementation.cache_tag}"
+    if _decode4.built_for != _tag:
+        raise ImportError(f"it was built for {_decode4.built_for}, this is {_tag}")
 except ImportError as e:
     raise ImportError(f"{PKG}/_decode4.so cannot be loaded: build it with `python {PKG}/build.py` "
-                      "(it is required; there is no fallback)") from e
+                      f"(it is required; there is no fallback): {e}") from e
 
 
 def _raw_stream(stream, index: int) -> int:
