@@ -25,14 +25,25 @@ import torch
 
 from ._lib import PKG, check, lib
 
+class _Missing:
+    """In the native module's place where it cannot be loaded: the rest of the
+    package does without it, every 4-bit operator raises."""
+
+    def __init__(self, why):
+        self._why = why
+
+    def __getattr__(self, name):
+        raise ImportError(f"{PKG}/_decode4.so cannot be loaded: build it with `python {PKG}/build.py` (the 4-bit "
+                          f"operators need it; there is no fallback): {self._why}")
+
+
 try:
     from . import _decode4
     _tag = f"torch {torch.__version__}, {sys.implementation.cache_tag}"
     if _decode4.built_for != _tag:
         raise ImportError(f"it was built for {_decode4.built_for}, this is {_tag}")
 except ImportError as e:
-    raise ImportError(f"{PKG}/_decode4.so cannot be loaded: build it with `python {PKG}/build.py` "
-                      f"(it is required; there is no fallback): {e}") from e
+    _decode4 = _Missing(str(e))
 
 
 def _raw_stream(stream, index: int) -> int:
@@ -71,6 +82,7 @@ class Linear4:
 
     def __init__(self, w: torch.Tensor | None = None, *, codes: torch.Tensor | None = None,
                  scales: torch.Tensor | None = None, stream=None):
+        _decode4.linear4_forward  # raises here if the module is missing
         h = ctypes.c_void_p(0)
         if w is not None:
             if codes is not None or scales is not None:
@@ -146,6 +158,7 @@ class KVCache4:
 
     def __init__(self, k_codes: torch.Tensor, k_scales: torch.Tensor, v_codes: torch.Tensor,
                  v_scales: torch.Tensor):
+        _decode4.kv4_attend  # raises here if the module is missing
         for t, dt, name in ((k_codes, torch.uint8, "k_codes"), (v_codes, torch.uint8, "v_codes"),
                             (k_scales, torch.float16, "k_scales"), (v_scales, torch.float16, "v_scales")):
             if not isinstance(t, torch.Tensor) or not t.is_cuda or t.dtype != dt:

@@ -1,5 +1,6 @@
 """The native module of the 4-bit operators' calls (_decode4.so): it is rebuilt,
-and not used, where it was compiled against another torch or Python."""
+and not used, where it was compiled against another torch or Python; and where
+it is missing those operators raise and the rest of the package works."""
 
 import importlib.util
 import os
@@ -41,3 +42,19 @@ def test_entry_of_another_torch_is_refused():
                  "except ImportError as e:\n"
                  "    print('refused:', e)\n")
     assert "refused:" in out and "built for torch" in out and "9.9.0" in out
+
+
+def test_package_without_the_entry(tmp_path):
+    pkg = tmp_path / "activation_sparse_swiglu_b200"
+    pkg.mkdir()
+    for name in os.listdir(PKG):
+        if name.endswith(".py") or name == "libprox.so":
+            os.symlink(os.path.join(PKG, name), pkg / name)
+    out = python("import activation_sparse_swiglu_b200 as p, activation_sparse_swiglu_b200.stack\n"
+                 "assert p.__file__.startswith(%r) and p.Layer and 'sm_100a' in p.version()\n"
+                 "for call in (lambda: p.plan_pages(*[None] * 7), p.Linear4, lambda: p.KVCache4(*[None] * 4)):\n"
+                 "    try:\n"
+                 "        call()\n"
+                 "    except ImportError as e:\n"
+                 "        print('refused:', e)\n" % str(tmp_path), tmp_path)
+    assert out.count("refused:") == 3 and out.count("_decode4.so cannot be loaded") == 3
