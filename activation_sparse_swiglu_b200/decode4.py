@@ -263,6 +263,21 @@ class PagePlan(NamedTuple):
     positions: torch.Tensor
     status: torch.Tensor
 
+    def per_request(self) -> "PagePlan":
+        """This plan of a step in which a request gains at most one token, with a
+        slot and a position for each request (cu None) in place of each new
+        token: slot -1 where a request gains none (idle, finished, rolled back;
+        all of them where the plan did not fit), position that of its newest
+        token.  On the current stream."""
+        if self.cu is None:
+            return self
+        positions = (self.lens - 1).clamp_(min=0)
+        if self.slots.numel() == 0:
+            return self._replace(cu=None, slots=torch.full_like(self.lens, -1, dtype=torch.int64), positions=positions)
+        at = self.cu[:-1].clamp(max=self.slots.numel() - 1).long()
+        slots = torch.where(self.cu[1:] > self.cu[:-1], self.slots.gather(0, at), -1)
+        return self._replace(cu=None, slots=slots, positions=positions)
+
 
 def plan_pages(lens: torch.Tensor, delta: torch.Tensor, table: torch.Tensor, free_pages: torch.Tensor,
                free_count: torch.Tensor, page_size: int, max_new: int, commit: bool = False,
@@ -308,11 +323,17 @@ class Attention4:
         self.rotate = rotate
 
     def step(self, x: torch.Tensor, plan: PagePlan, table: torch.Tensor, stream=None) -> torch.Tensor:
-        """x [B, d], one new token of each request (B <= 16), under a plan in
-        which every request gains one -> [B, d]."""
+        """x [B, d], the new token of each request (B <= 16) -> [B, d].  A request
+        may gain none in the plan (idle, finished): its row of x is not cached
+        and attends to what it has (zeros if that is nothing).  More than one
+        is not looked for (the plan is on the device): verify drafted tokens
+        with the operators themselves.  A plan whose status is 1 caches
+        nothing.  Calls for several layers share plan.per_request(), which each
+        would work out again."""
         if stream is not None:  # what the step makes on the way belongs to its stream
             with on_stream(stream, self.qkv.device):
                 return self.step(x, plan, table)
+        plan = plan.per_request()
         B, D = x.shape[0], self.head_dim
         heads = self.qkv.forward(x).view(B, self.n_heads + 2 * self.n_kv_heads, D)
         q, k, v = heads.split_with_sizes([self.n_heads, self.n_kv_heads, self.n_kv_heads], 1)

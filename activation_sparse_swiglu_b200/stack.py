@@ -148,15 +148,19 @@ class Stack:
 
     def decode(self, x: torch.Tensor, plan, table: torch.Tensor, stream=None) -> torch.Tensor:
         """One decode step of B requests through attention and FFN of every
-        layer, each chained to the next through unit-gain RMSNorm: x [B, d] the
-        requests' new tokens, plan the plan_pages() result in which every
-        request gains one token, table its page table.  Returns the last
-        layer's output [B, d]."""
+        layer, chained as forward() chains the FFNs: each sub-layer's output
+        through unit-gain RMSNorm into the next, without residuals.  x: fp32
+        [B, d], the requests' new tokens (normalised as the first layer wants
+        them); plan: the plan_pages() result in which each request gains at most
+        one token (one that gains none is not cached, see Attention4.step; the
+        status is the caller's to check); table: its page table.  Returns the
+        last layer's output [B, d]."""
         if self.attention is None:
             raise RuntimeError("the stack has no attention sub-layers")
         if stream is not None:  # what the step makes on the way belongs to its stream
             with on_stream(stream, x.device):
                 return self.decode(x, plan, table)
+        plan = plan.per_request()
         y = None
         for li, (attn, layer) in enumerate(zip(self.attention, self.layers)):
             if li > 0:
