@@ -75,6 +75,7 @@ class Stack:
                        for (wg, wu, wd) in weights]
         self.taus = [0.0] * len(self.layers)
         self.k = k
+        self.max_batch = max_batch
 
     def calibrate(self, x_cal: torch.Tensor, s1: float, s2: float | None = None, stream=None):
         """Algorithm 1 on fp32 calibration tokens [n, d] (n <= max_batch).
@@ -157,6 +158,11 @@ class Stack:
         last layer's output [B, d]."""
         if self.attention is None:
             raise RuntimeError("the stack has no attention sub-layers")
+        # (a call that a later sub-layer would refuse must not have cached rows)
+        if not isinstance(x, torch.Tensor) or not x.is_cuda or x.dtype != torch.float32:
+            raise TypeError("x must be a float32 CUDA tensor")
+        if x.dim() != 2 or not 1 <= x.shape[0] <= self.max_batch:
+            raise ValueError(f"x must be [B, d] of 1 to max_batch={self.max_batch} requests, got {tuple(x.shape)}")
         if stream is not None:  # what the step makes on the way belongs to its stream
             with on_stream(stream, x.device):
                 return self.decode(x, plan, table)

@@ -1,4 +1,5 @@
-"""Decode steps under plans in which not every request gains a token."""
+"""Decode steps under plans in which not every request gains a token, and calls
+that a step refuses before it has changed anything."""
 
 import pytest
 import torch
@@ -97,6 +98,24 @@ def test_plan_that_does_not_fit_caches_nothing():
         assert int(plan.status) == 1
         stack.decode(torch.randn((2, D_MODEL), device="cuda"), plan, table)
         assert all(torch.equal(a, b) for a, b in zip(tensors(stack), before))
+
+
+def test_steps_are_refused_before_they_change_anything():
+    stack = build(1, max_batch=2)
+    table, lens = torch.arange(3, dtype=torch.int32, device="cuda").view(3, 1), i32(1, 1, 1)
+    plan = prox.PagePlan(lens, None, None, torch.arange(3, device="cuda") * PAGE, lens - 1, None)
+    two = prox.PagePlan(lens[:2], None, None, plan.slots[:2], plan.positions[:2], None)
+    before = [t.clone() for t in tensors(stack)]
+    x = torch.randn((3, D_MODEL), device="cuda")
+    for bad, kind, args in ((x, ValueError, (plan, table)), (x[:2].half(), TypeError, (two, table[:2])),
+                            (x[:2].cpu(), TypeError, (two, table[:2])), (x[0], ValueError, (two, table[:2])),
+                            (x[:0], ValueError, (two, table[:2]))):
+        for stream in (None, torch.cuda.Stream()):
+            with pytest.raises(kind):
+                stack.decode(bad, *args, stream=stream)
+    assert all(torch.equal(a, b) for a, b in zip(tensors(stack), before))
+    stack.decode(x[:2], two, table[:2])
+    assert not torch.equal(tensors(stack)[0], before[0])
 
 
 def test_per_request_in_a_captured_step():
