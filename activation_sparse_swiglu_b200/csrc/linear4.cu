@@ -38,8 +38,10 @@
 // distributed shared memory in rank order, so results do not depend on timing
 // and no scratch in global memory is shared between calls.
 //
-// Bound: HBM at large sizes (0.52 bytes per weight), launch and one pass of
-// load latency at small ones.
+// Bound: HBM at large sizes (0.52 bytes per weight; 5120 x 131072 at one token
+// 58 us, 0.91 of the copy bandwidth), issue and the tensor pipe from 9 tokens on
+// (two column tiles: 82.6 us at 16), launch and one pass of load latency at small
+// ones (4096 x 6144 at one token 5.8 us).
 #include "decode4.h"
 #include "quant4.cuh"
 
@@ -541,7 +543,7 @@ int col_tiles(int B, int dtype) {
 
 // Units in flight per warp: 4 cover a small matrix's whole share at once; 3 or
 // 2 where x takes the room.  (With one, 16 tokens x 5120 ran at HBM's latency:
-// 83 us for 131072 channels.)
+// 83 us for 131072 channels, when two or three took 76.5.)
 template <int PF>
 Kernel pick_depth(int dtype, int nt) {
   switch (dtype) {
@@ -567,10 +569,10 @@ size_t ring_bytes(int nt, int depth) { return (size_t)warps_of(nt) * depth * kSl
 // codes each, about 90 SM cycles at the copy bandwidth), plus what converting x
 // costs (15 cycles per column and group), plus what a launch in clusters and
 // the join across them costs, plus 30 per extra phase of x (the rings run dry).
-// Measured at 4096 x 4096, clusters of 1 / 2 / 4 / 8: one token 5.1 / 6.4 / 6.8
-// / 8.2 us, 16 tokens 9.2 / 9.3 / 9.4 / 10.8; at 8192 x 1024 6.0 / 5.5 / 5.8 /
-// 6.5 and 17.9 / 9.8 / 8.0 / 8.1; at 28672 x 8192 with 16 tokens 96 / 64 / 48 /
-// 43.
+// Measured for bf16 tokens, clusters of 1 / 2 / 4 / 8: at 4096 x 4096 one token
+// 4.4 / 5.7 / 6.2 / 8.5 us, 16 tokens 8.3 / 8.5 / 8.7 / 10.6; at 8192 x 1024 5.0 /
+// 4.7 / 5.2 / 5.8 and 15.8 / 8.8 / 7.0 / 7.3; at 28672 x 8192 with 16 tokens 87 /
+// 62 / 49 / 44 (16 fp32 tokens: 174 / 114 / 79 / 75).
 constexpr double kJoin[4] = {0, 35, 45, 75};
 
 bool plan_linear4(const prox_linear4* L, int strips, int B, int dtype, Plan* best) {
