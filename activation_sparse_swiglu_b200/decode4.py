@@ -335,6 +335,10 @@ class Attention4:
                 return self.step(x, plan, table)
         plan = plan.per_request()
         B, D = x.shape[0], self.head_dim
+        # (what attend would refuse must not have cached rows)
+        if x.dim() != 2 or plan.lens.numel() != B or plan.slots.numel() < B or table.dim() != 2 or table.shape[0] != B:
+            raise ValueError(f"x {tuple(x.shape)}, a plan of {plan.lens.numel()} requests and a table "
+                             f"{tuple(table.shape)} do not belong together")
         heads = self.qkv.forward(x).view(B, self.n_heads + 2 * self.n_kv_heads, D)
         q, k, v = heads.split_with_sizes([self.n_heads, self.n_kv_heads, self.n_kv_heads], 1)
         if self.rotate is not None:

@@ -118,6 +118,25 @@ def test_steps_are_refused_before_they_change_anything():
     assert not torch.equal(tensors(stack)[0], before[0])
 
 
+def test_steps_of_other_sizes_than_their_plan_are_refused():
+    """Before a row is cached: fewer or more requests in x, plan or table."""
+    stack = build(1)
+    table, lens = torch.arange(4, dtype=torch.int32, device="cuda").view(4, 1), i32(1, 1, 1, 1)
+    free, count = i32(9, 9, 9, 9), i32(0)
+    before = [t.clone() for t in tensors(stack)]
+    x = torch.randn((4, D_MODEL), device="cuda")
+    by_hand = prox.PagePlan(lens, None, None, torch.arange(4, device="cuda") * PAGE, lens - 1, None)
+    for plan in (by_hand, prox.plan_pages(lens, lens, table, free, count, PAGE, max_new=4)):
+        for bad in ((x[:3], plan, table), (x[:3], plan, table[:3]), (x, plan, table[:3]), (x[0], plan, table),
+                    (x, plan, table[:, 0]), (x, plan._replace(cu=None, slots=plan.slots[:3]), table)):
+            for stream in (None, torch.cuda.Stream()):
+                with pytest.raises(ValueError):
+                    stack.attention[0].step(*bad, stream=stream)
+                with pytest.raises(ValueError):
+                    stack.decode(*bad, stream=stream)
+    assert all(torch.equal(a, b) for a, b in zip(tensors(stack), before))
+
+
 def test_per_request_in_a_captured_step():
     """A captured step replays on another plan: nothing of it is on the host."""
     stack = build(1)
