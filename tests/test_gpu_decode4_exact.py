@@ -167,11 +167,12 @@ def test_attend_non_finite_query_leaves_its_block_as_it_was(bad, G, Tq, D, dtype
 
 @pytest.mark.parametrize("dtype", ref.TYPES)
 @pytest.mark.parametrize("D", [64, 128, 256])
-def test_attend_heads_of_very_different_size(D, dtype):
+@pytest.mark.parametrize("Tq", [1, 3])
+def test_attend_heads_of_very_different_size(Tq, D, dtype):
     """Heads of one group whose queries differ by many orders: each is as good
     as alone, at the scale that brings its scores to the usual size."""
     steps = [0, 8, 16] if dtype == torch.float16 else [0, 20, 40, 60]
-    cache, q, table, lens = attend_case(prox, [300, 33], 1, 2, len(steps), D, 32, torch.float32, seed=D + 3)
+    cache, q, table, lens = attend_case(prox, [300, 33], Tq, 2, len(steps), D, 32, torch.float32, seed=D + 3)
     for j, e in enumerate(steps):
         q[:, :, j::len(steps)] *= 2.0 ** -e
     q = q.to(dtype)
